@@ -26,9 +26,13 @@ __all__ = [
     "fp8bw_status_string", "fp8bw_last_device_error", "fp8bw_version",
     "fp8bw_selftest_wait_timeout",
     "linear_fprop", "linear_dgrad", "linear_wgrad",
+    "FEW_TOKENS", "MAX_EXPERTS", "MAX_CHOICES",
+    "fp8_linear_few", "fp8_moe_route", "fp8_moe_route_bwd", "fp8_moe_plan_rows", "fp8_moe_plan",
+    "fp8_gemm_grouped", "fp8_gemm_grouped_wgrad_acc32", "fp8_moe_few", "fp8_moe_few_workspace",
 ]
 
 FPROP, DGRAD, WGRAD = 0, 1, 2
+FEW_TOKENS, MAX_EXPERTS, MAX_CHOICES = 64, 1024, 32  # the limits of include/fp8bw.h
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libfp8bw.so")
@@ -62,6 +66,21 @@ def lib():
         L.fp8_quant_act_dual_e8m0.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp]
         L.fp8_quant_weight_e8m0.argtypes = [vp, i64, i64, vp, vp, vp, vp]
         L.fp8_gemm_blockwise_e8m0.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        L.fp8_linear_few.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        L.fp8_moe_route.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+        L.fp8_moe_route_bwd.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, vp]
+        L.fp8_moe_plan.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.fp8_gemm_grouped.argtypes = [i32, vp, vp, vp, vp, vp, i64, vp, i64, i64, i64, vp]
+        L.fp8_gemm_grouped_wgrad_acc32.argtypes = [vp, vp, vp, vp, vp, i64, vp, i64, i64, i64, vp]
+        L.fp8_moe_few.argtypes = [vp] * 8 + [i64] * 5 + [vp, vp]
+        for f in (L.fp8_moe_plan_rows, L.fp8_moe_plan_workspace):
+            f.argtypes = [i64, i64, i64]
+            f.restype = i64
+        L.fp8_moe_few_workspace.argtypes = [i64, i64, i64, i64]
+        L.fp8_moe_few_workspace.restype = i64
+        for f in (L.fp8_linear_few, L.fp8_moe_route, L.fp8_moe_route_bwd, L.fp8_moe_plan,
+                  L.fp8_gemm_grouped, L.fp8_gemm_grouped_wgrad_acc32, L.fp8_moe_few):
+            f.restype = i32
         for f in (L.fp8_quant_act, L.fp8_quant_act_t, L.fp8_quant_act_dual, L.fp8_quant_weight,
                   L.fp8_gemm_blockwise, L.fp8_gemm_wgrad_acc32, L.fp8_quant_act_e8m0,
                   L.fp8_quant_act_t_e8m0, L.fp8_quant_act_dual_e8m0, L.fp8_quant_weight_e8m0,
@@ -425,3 +444,245 @@ def linear_wgrad(dy, x, stream=None):
     qdyt, sdyt = fp8_quant_act_t(dy, stream=stream)
     qxt, sxt = fp8_quant_act_t(x, stream=stream)
     return fp8_gemm_blockwise(WGRAD, qdyt, sdyt, qxt, sxt, Dout, Din, T, stream=stream)
+
+
+# -- few tokens: the linear of a decode step --------------------------------------
+
+def fp8_linear_few(x, qw, sw, out=None, stream=None):
+    """Y[M][N] bf16 = X W^T for X[M][K] bf16 with 1 <= M <= FEW_TOKENS tokens and a weight
+    quantized by fp8_quant_weight; X is quantized inside the call as by fp8_quant_act."""
+    import torch
+    M, K = _few_rows(x, "x")
+    if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
+        raise ValueError("qw must be a 2-D tensor")
+    N = int(qw.shape[0])
+    _dims(N)
+    dev = _validate([(x, torch.bfloat16, (M, K), "x"), (qw, torch.uint8, (N, K), "qw"),
+                     (sw, torch.float32, (N // 128, K // 128), "sw"),
+                     (out, torch.bfloat16, (M, N), "out")])
+    with _on(dev):
+        out = _alloc(out, (M, N), torch.bfloat16, dev)
+        _check(lib().fp8_linear_few(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), out.data_ptr(),
+                                    M, N, K, _stream(stream)), "fp8_linear_few")
+    return out
+
+
+def _few_rows(x, name):
+    """Rows and columns of a few-token activation."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    M, K = int(x.shape[0]), int(x.shape[1])
+    if not 1 <= M <= FEW_TOKENS:
+        raise ValueError(f"{name} has {M} tokens, expected 1 to {FEW_TOKENS}")
+    _dims(K)
+    return M, K
+
+
+# -- mixture of experts -----------------------------------------------------------
+
+def _experts(T, E, k):
+    if T < 1:
+        raise ValueError(f"token count {T} is not positive")
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"{E} experts, expected 1 to {MAX_EXPERTS}")
+    if not 1 <= k <= min(E, MAX_CHOICES):
+        raise ValueError(f"{k} choices per token, expected 1 to {min(E, MAX_CHOICES)}")
+
+
+def _logits(logits, k):
+    """Sizes of a router call: (T, E, k, whether the logits are bf16)."""
+    import torch
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    T, E, k = int(logits.shape[0]), int(logits.shape[1]), int(k)
+    _experts(T, E, k)
+    return T, E, k, logits.dtype == torch.bfloat16
+
+
+def fp8_moe_route(logits, k: int, renorm: bool = True, weights=None, ids=None, stream=None):
+    """logits[T][E] (float32 or bf16) -> (weights[T][k] float32, ids[T][k] int32): the k
+    largest, ties to the lowest expert, with softmax weights over the chosen experts
+    (renorm) or over all.  -inf and NaN are never chosen (id -1, weight 0)."""
+    import torch
+    T, E, k, bf16 = _logits(logits, k)
+    dev = _validate([(logits, logits.dtype, (T, E), "logits"),
+                     (weights, torch.float32, (T, k), "weights"), (ids, torch.int32, (T, k), "ids")])
+    with _on(dev):
+        weights = _alloc(weights, (T, k), torch.float32, dev)
+        ids = _alloc(ids, (T, k), torch.int32, dev)
+        _check(lib().fp8_moe_route(logits.data_ptr(), int(bf16), T, E, k, int(bool(renorm)),
+                                   weights.data_ptr(), ids.data_ptr(), _stream(stream)),
+               "fp8_moe_route")
+    return weights, ids
+
+
+def fp8_moe_route_bwd(dweights, weights, ids, logits, renorm: bool = True, dlogits=None,
+                      stream=None):
+    """Gradient of the logits (of their type) from that of the weights; weights, ids,
+    logits and renorm as in the forward call."""
+    import torch
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor")
+    T, E, k, bf16 = _logits(logits, ids.shape[1])
+    dev = _validate([(dweights, torch.float32, (T, k), "dweights"),
+                     (weights, torch.float32, (T, k), "weights"), (ids, torch.int32, (T, k), "ids"),
+                     (logits, logits.dtype, (T, E), "logits"),
+                     (dlogits, logits.dtype, (T, E), "dlogits")])
+    with _on(dev):
+        dlogits = _alloc(dlogits, (T, E), logits.dtype, dev)
+        _check(lib().fp8_moe_route_bwd(dweights.data_ptr(), weights.data_ptr(), ids.data_ptr(),
+                                       logits.data_ptr(), int(bf16), T, E, k, int(bool(renorm)),
+                                       dlogits.data_ptr(), _stream(stream)), "fp8_moe_route_bwd")
+    return dlogits
+
+
+def fp8_moe_plan_rows(T: int, E: int, k: int) -> int:
+    """Rows of the layout by expert that hold any split of T * k pairs over E experts."""
+    T, E, k = int(T), int(E), int(k)
+    _experts(T, E, k)
+    rows = int(lib().fp8_moe_plan_rows(T, E, k))
+    if rows == 0:
+        raise ValueError(f"{T} tokens with {k} choices exceed the largest layout")
+    return rows
+
+
+def fp8_moe_plan(ids, E: int, seg=None, row=None, src=None, workspace=None, stream=None):
+    """ids[T][k] int32 -> (seg[E + 1], row[T][k], src[rows]) int32: expert e owns the blocks of
+    128 rows seg[e] .. seg[e + 1] - 1; row is each pair's row (-1: left out), src each row's
+    pair t * k + j (-1: none).  workspace: uint8, at least what the header asks for."""
+    import torch
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor")
+    T, k, E = int(ids.shape[0]), int(ids.shape[1]), int(E)
+    rows = fp8_moe_plan_rows(T, E, k)
+    dev = _validate([(ids, torch.int32, (T, k), "ids"), (seg, torch.int32, (E + 1,), "seg"),
+                     (row, torch.int32, (T, k), "row"), (src, torch.int32, (rows,), "src")])
+    need = int(lib().fp8_moe_plan_workspace(T, E, k))
+    with _on(dev):
+        seg = _alloc(seg, (E + 1,), torch.int32, dev)
+        row = _alloc(row, (T, k), torch.int32, dev)
+        src = _alloc(src, (rows,), torch.int32, dev)
+        workspace = _workspace(workspace, need, dev, stream)
+        _check(lib().fp8_moe_plan(ids.data_ptr(), T, E, k, seg.data_ptr(), row.data_ptr(),
+                                  src.data_ptr(), workspace.data_ptr(), _stream(stream)),
+               "fp8_moe_plan")
+    return seg, row, src
+
+
+def _workspace(ws, need, dev, stream):
+    """The caller's workspace, checked, or one of this call's own.  It is freed when the
+    call returns, so it has to come from the allocator's pool of the stream that uses it."""
+    import torch
+    if ws is None:
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
+        raise TypeError("workspace must be a uint8 tensor")
+    if ws.dim() != 1 or ws.numel() < need:
+        raise ValueError(f"workspace has shape {tuple(ws.shape)}, expected ({need},) or longer")
+    _validate([(ws, torch.uint8, ws.shape, "workspace")])
+    if ws.device != dev:
+        raise ValueError(f"workspace is on {ws.device}, expected {dev} (one device per call)")
+    return ws
+
+
+def _grouped_shapes(mode, M, N, K, seg):
+    """Operand shapes of a grouped GEMM (include/fp8bw.h): E, a, sa, b, sb, d."""
+    import torch
+    if mode not in (FPROP, DGRAD, WGRAD):
+        raise ValueError(f"mode must be FPROP, DGRAD or WGRAD, got {mode}")
+    if not isinstance(seg, torch.Tensor) or seg.dim() != 1 or seg.numel() < 2:
+        raise ValueError("seg must be a 1-D tensor of E + 1 block offsets")
+    E = int(seg.numel()) - 1
+    if E > MAX_EXPERTS:
+        raise ValueError(f"{E} experts, expected 1 to {MAX_EXPERTS}")
+    _dims(M, N, K)
+    a, sa = (M, K), (K // 128, M)
+    if mode == WGRAD:
+        return E, a, sa, (N, K), (K // 128, N), (E, M, N)
+    r, c = (N, K) if mode == FPROP else (K, N)
+    return E, a, sa, (E, r, c), (E, r // 128, c // 128), (M, N)
+
+
+def fp8_gemm_grouped(mode: int, a, sa, b, sb, seg, M: int, N: int, K: int, out=None, stream=None):
+    """fp8_gemm_blockwise with one weight per expert: expert e owns the 128-token blocks
+    seg[e] .. seg[e + 1] - 1 (see fp8_moe_plan and include/fp8bw.h).  FPROP and DGRAD give
+    [M][N] and leave the rows of blocks that no expert owns as they were; WGRAD gives
+    [E][M][N]."""
+    import torch
+    M, N, K = int(M), int(N), int(K)
+    E, sh_a, sh_sa, sh_b, sh_sb, sh_d = _grouped_shapes(mode, M, N, K, seg)
+    dev = _validate([(a, torch.uint8, sh_a, "a"), (sa, torch.float32, sh_sa, "sa"),
+                     (b, torch.uint8, sh_b, "b"), (sb, torch.float32, sh_sb, "sb"),
+                     (seg, torch.int32, (E + 1,), "seg"), (out, torch.bfloat16, sh_d, "out")])
+    with _on(dev):
+        out = _alloc(out, sh_d, torch.bfloat16, dev)
+        _check(lib().fp8_gemm_grouped(int(mode), a.data_ptr(), sa.data_ptr(), b.data_ptr(),
+                                      sb.data_ptr(), seg.data_ptr(), E, out.data_ptr(), M, N, K,
+                                      _stream(stream)), "fp8_gemm_grouped")
+    return out
+
+
+def fp8_gemm_grouped_wgrad_acc32(a, sa, b, sb, seg, M: int, N: int, K: int, dw32, stream=None):
+    """dw32[E][M][N] (float32, caller-owned) += the grouped WGRAD, kept in FP32."""
+    import torch
+    M, N, K = int(M), int(N), int(K)
+    E, sh_a, sh_sa, sh_b, sh_sb, sh_d = _grouped_shapes(WGRAD, M, N, K, seg)
+    if dw32 is None:
+        raise TypeError("dw32 must be a caller-owned float32 tensor")
+    dev = _validate([(a, torch.uint8, sh_a, "a"), (sa, torch.float32, sh_sa, "sa"),
+                     (b, torch.uint8, sh_b, "b"), (sb, torch.float32, sh_sb, "sb"),
+                     (seg, torch.int32, (E + 1,), "seg"), (dw32, torch.float32, sh_d, "dw32")])
+    with _on(dev):
+        _check(lib().fp8_gemm_grouped_wgrad_acc32(a.data_ptr(), sa.data_ptr(), b.data_ptr(),
+                                                  sb.data_ptr(), seg.data_ptr(), E,
+                                                  dw32.data_ptr(), M, N, K, _stream(stream)),
+               "fp8_gemm_grouped_wgrad_acc32")
+    return dw32
+
+
+def fp8_moe_few_workspace(T: int, k: int, H: int, I: int) -> int:
+    """Bytes of workspace that fp8_moe_few needs."""
+    need = int(lib().fp8_moe_few_workspace(int(T), int(k), int(H), int(I)))
+    if need == 0:
+        raise ValueError(f"no few-token layer of {T} tokens, {k} choices, sizes {H} and {I}")
+    return need
+
+
+def fp8_moe_few(x, w1, s1, w2, s2, ids, weights, out=None, workspace=None, stream=None):
+    """Y[T][H] bf16: all experts of a SwiGLU layer for X[T][H] bf16, 1 <= T <= FEW_TOKENS.
+    w1[E][2I][H] (gate rows, then up rows) with s1[E][2I/128][H/128] and w2[E][H][I] with
+    s2[E][H/128][I/128] as fp8_quant_weight gives them; ids, weights[T][k] as from
+    fp8_moe_route.  workspace: uint8, fp8_moe_few_workspace(T, k, H, I) bytes or more, one
+    for each call (or captured graph) that may run at the same time."""
+    import torch
+    T, H = _few_rows(x, "x")
+    for t, name in ((w1, "w1"), (w2, "w2")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a 3-D tensor")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor")
+    E, I, k = int(w2.shape[0]), int(w2.shape[2]), int(ids.shape[1])
+    _dims(I)
+    _experts(T, E, k)
+    dev = _validate([(x, torch.bfloat16, (T, H), "x"),
+                     (w1, torch.uint8, (E, 2 * I, H), "w1"),
+                     (s1, torch.float32, (E, 2 * I // 128, H // 128), "s1"),
+                     (w2, torch.uint8, (E, H, I), "w2"),
+                     (s2, torch.float32, (E, H // 128, I // 128), "s2"),
+                     (ids, torch.int32, (T, k), "ids"),
+                     (weights, torch.float32, (T, k), "weights"),
+                     (out, torch.bfloat16, (T, H), "out")])
+    with _on(dev):
+        out = _alloc(out, (T, H), torch.bfloat16, dev)
+        workspace = _workspace(workspace, fp8_moe_few_workspace(T, k, H, I), dev, stream)
+        _check(lib().fp8_moe_few(x.data_ptr(), w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
+                                 s2.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                                 out.data_ptr(), T, E, k, H, I, workspace.data_ptr(),
+                                 _stream(stream)), "fp8_moe_few")
+    return out

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "fp8bw.h"
+#include "moe.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -85,6 +86,47 @@ bool dim_ok(int64_t d)
 bool tok_ok(int64_t d)
 {
     return d > 0 && d <= FP8BW_MAX_DIM && (d % 16) == 0;
+}
+
+bool all_aligned16(std::initializer_list<const void *> ptrs)
+{
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return false;
+    return true;
+}
+
+bool none_null(std::initializer_list<const void *> ptrs)
+{
+    for (const void *p : ptrs)
+        if (!p)
+            return false;
+    return true;
+}
+
+bool experts_ok(int64_t E)
+{
+    return E > 0 && E <= FP8BW_MAX_EXPERTS;
+}
+
+// Tokens, experts and choices of a mixture-of-experts call.
+bool choices_ok(int64_t T, int64_t E, int64_t k)
+{
+    return T > 0 && T <= FP8BW_MAX_DIM && experts_ok(E) && k > 0 && k <= E && k <= FP8BW_MAX_CHOICES;
+}
+
+bool plan_ok(int64_t T, int64_t E, int64_t k)
+{
+    return choices_ok(T, E, k) && fp8bw::moe_plan_rows(T, int(k), int(E)) <= FP8BW_MAX_DIM;
+}
+
+// Rows of the experts' matrices, stacked: tensor-map coordinates are 32-bit.
+constexpr int64_t kMaxStacked = int64_t(1) << 30;
+
+bool few_ok(int64_t T, int64_t k, int64_t H, int64_t I)
+{
+    return T > 0 && T <= FP8BW_FEW_TOKENS && k > 0 && k <= FP8BW_MAX_CHOICES && dim_ok(H) &&
+           dim_ok(I);
 }
 
 int from_cuda(cudaError_t e)
@@ -265,6 +307,148 @@ int fp8_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b, co
                                                     static_cast<cudaStream_t>(stream), sms));
 }
 
+// ---- few tokens and mixture of experts ----
+
+int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void *y_bf16, int64_t M,
+                   int64_t N, int64_t K, void *stream)
+{
+    if (!none_null({x_bf16, qw, sw, y_bf16}))
+        return FP8BW_EINVAL;
+    if (M <= 0 || M > FP8BW_FEW_TOKENS || !dim_ok(N) || !dim_ok(K))
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({x_bf16, qw, sw, y_bf16}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({x_bf16, qw, sw, y_bf16}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_linear_few(x_bf16, int(M), qw, sw, y_bf16, N, K,
+                                              static_cast<cudaStream_t>(stream), sms));
+}
+
+int fp8_moe_route(const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
+                  float *weights, int32_t *ids, void *stream)
+{
+    if (!none_null({logits, weights, ids}))
+        return FP8BW_EINVAL;
+    if (!choices_ok(T, E, k))
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({logits, weights, ids}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({logits, weights, ids}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_moe_route(logits, bf16 != 0, T, int(E), int(k), renorm != 0,
+                                             weights, ids, static_cast<cudaStream_t>(stream), sms));
+}
+
+int fp8_moe_route_bwd(const float *dweights, const float *weights, const int32_t *ids,
+                      const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
+                      void *dlogits, void *stream)
+{
+    if (!none_null({dweights, weights, ids, logits, dlogits}))
+        return FP8BW_EINVAL;
+    if (!choices_ok(T, E, k))
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({dweights, weights, ids, logits, dlogits}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({dweights, weights, ids, logits, dlogits}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_moe_route_bwd(dweights, weights, ids, logits, bf16 != 0, T, int(E),
+                                                 int(k), renorm != 0, dlogits,
+                                                 static_cast<cudaStream_t>(stream), sms));
+}
+
+int64_t fp8_moe_plan_rows(int64_t T, int64_t E, int64_t k)
+{
+    return plan_ok(T, E, k) ? fp8bw::moe_plan_rows(T, int(k), int(E)) : 0;
+}
+
+int64_t fp8_moe_plan_workspace(int64_t T, int64_t E, int64_t k)
+{
+    return plan_ok(T, E, k) ? int64_t(fp8bw::moe_plan_workspace(T, int(k), int(E))) : 0;
+}
+
+int fp8_moe_plan(const int32_t *ids, int64_t T, int64_t E, int64_t k, int32_t *seg, int32_t *row,
+                 int32_t *src, void *workspace, void *stream)
+{
+    if (!none_null({ids, seg, row, src, workspace}))
+        return FP8BW_EINVAL;
+    if (!plan_ok(T, E, k))
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({ids, seg, row, src, workspace}))
+        return FP8BW_EALIGN;
+    int st;
+    if (device_sms({ids, seg, row, src, workspace}, &st) < 0)
+        return st;
+    return from_cuda(fp8bw::launch_moe_plan(ids, T, int(k), int(E), seg, row, src, workspace,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int fp8_gemm_grouped(int mode, const uint8_t *a, const float *sa, const uint8_t *b, const float *sb,
+                     const int32_t *seg, int64_t E, void *d_bf16, int64_t M, int64_t N, int64_t K,
+                     void *stream)
+{
+    if (mode < FP8BW_FPROP || mode > FP8BW_WGRAD || !none_null({a, sa, b, sb, seg, d_bf16}))
+        return FP8BW_EINVAL;
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K) || !experts_ok(E) ||
+        E * (mode == FP8BW_WGRAD ? M : N > K ? N : K) > kMaxStacked)
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({a, sa, b, sb, seg, d_bf16}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({a, sa, b, sb, seg, d_bf16}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_gemm_grouped(mode, a, sa, b, sb, d_bf16, seg, int(E), M, N, K,
+                                                static_cast<cudaStream_t>(stream), sms));
+}
+
+int fp8_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b,
+                                 const float *sb, const int32_t *seg, int64_t E, float *dw32,
+                                 int64_t M, int64_t N, int64_t K, void *stream)
+{
+    if (!none_null({a, sa, b, sb, seg, dw32}))
+        return FP8BW_EINVAL;
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K) || !experts_ok(E) || E * M > kMaxStacked)
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({a, sa, b, sb, seg, dw32}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({a, sa, b, sb, seg, dw32}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_gemm_grouped_wgrad_acc32(a, sa, b, sb, dw32, seg, int(E), M, N, K,
+                                                            static_cast<cudaStream_t>(stream), sms));
+}
+
+int64_t fp8_moe_few_workspace(int64_t T, int64_t k, int64_t H, int64_t I)
+{
+    return few_ok(T, k, H, I) ? int64_t(fp8bw::moe_few_workspace(int(T), int(k), H, I)) : 0;
+}
+
+int fp8_moe_few(const void *x_bf16, const uint8_t *w1, const float *s1, const uint8_t *w2,
+                const float *s2, const int32_t *ids, const float *weights, void *y_bf16, int64_t T,
+                int64_t E, int64_t k, int64_t H, int64_t I, void *workspace, void *stream)
+{
+    if (!none_null({x_bf16, w1, s1, w2, s2, ids, weights, y_bf16, workspace}))
+        return FP8BW_EINVAL;
+    if (!few_ok(T, k, H, I) || !choices_ok(T, E, k) || E * 2 * I > kMaxStacked || E * H > kMaxStacked)
+        return FP8BW_ESHAPE;
+    if (!all_aligned16({x_bf16, w1, s1, w2, s2, ids, weights, y_bf16, workspace}))
+        return FP8BW_EALIGN;
+    int st;
+    const int sms = device_sms({x_bf16, w1, s1, w2, s2, ids, weights, y_bf16, workspace}, &st);
+    if (sms < 0)
+        return st;
+    return from_cuda(fp8bw::launch_moe_few(x_bf16, int(T), w1, s1, w2, s2, ids, weights, int(k),
+                                           int(E), H, I, y_bf16, workspace,
+                                           static_cast<cudaStream_t>(stream), sms));
+}
+
 const char *fp8bw_status_string(int status)
 {
     switch (status) {
@@ -285,12 +469,13 @@ int fp8bw_last_device_error(void *stream)
     int st;
     if (device_sms({}, &st) < 0)
         return st;
-    int v = 0, w = 0, u = 0;
+    int v = 0, w = 0, u = 0, f = 0;
     if (fp8bw::read_and_clear_device_error(static_cast<cudaStream_t>(stream), &v) != cudaSuccess ||
         fp8bw::read_and_clear_mx_error(&w) != cudaSuccess ||
-        fp8bw::read_and_clear_quant_error(&u) != cudaSuccess)
+        fp8bw::read_and_clear_quant_error(&u) != cudaSuccess ||
+        fp8bw::read_and_clear_few_error(&f) != cudaSuccess)
         return FP8BW_ECUDA;
-    return (v || w || u) ? FP8BW_ETIMEOUT : FP8BW_OK;
+    return (v || w || u || f) ? FP8BW_ETIMEOUT : FP8BW_OK;
 }
 
 int fp8bw_selftest_wait_timeout(int64_t limit_us, void *stream)

@@ -54,7 +54,9 @@ constexpr uint64_t DRAIN_NS = 20000000ull;
 
 enum : int { ERR_PRODUCER = 1, ERR_MMA_FULL = 2, ERR_MMA_TEMPTY = 3, ERR_EPI = 4, ERR_SCALES = 5 };
 
-template <int BN_, int MODE_, int STAGES_, int CG_, bool OUT32_ = false>
+constexpr int MAX_GROUPS = 1024;  // experts of a grouped GEMM
+
+template <int BN_, int MODE_, int STAGES_, int CG_, bool OUT32_ = false, bool GROUPED_ = false>
 struct GemmCfg {
     static constexpr int BN = BN_;      // columns of D per tile (both CTAs of a pair)
     static constexpr int MODE = MODE_;  // 0 fprop, 1 dgrad (B is MN-major), 2 wgrad
@@ -63,6 +65,9 @@ struct GemmCfg {
     // OUT32: instead of storing BF16, add the FP32 sum into an FP32 output (wgrad
     // main-grad accumulation; TMA reduce-add on the pair path)
     static constexpr bool OUT32 = OUT32_;
+    // GROUPED: one weight (wgrad: one output) per expert, which owns a run of 128-row
+    // blocks; see GroupTable
+    static constexpr bool GROUPED = GROUPED_;
     static constexpr int TILE_M = BM * CG;
     static constexpr int EPI_WARPS = 8;
     static constexpr int COLS = 4 * BN / EPI_WARPS;  // columns per epilogue thread
@@ -108,7 +113,9 @@ struct GemmCfg {
     static constexpr int OUT_BYTES = TMA_STORE ? EPI_WARPS * STAGE_OUT_WARP : 0;
     static constexpr int RING_OFF = STAGES * STAGE_BYTES + OUT_BYTES;
     static constexpr int BAR_OFF = RING_OFF + RING_BYTES;
-    static constexpr int SMEM = 1024 + BAR_OFF + 512;
+    static constexpr int TABLE_OFF = BAR_OFF + 512;
+    static constexpr int TABLE_BYTES = GROUPED ? 2 * (MAX_GROUPS + 1) * 4 : 0;
+    static constexpr int SMEM = 1024 + TABLE_OFF + TABLE_BYTES;
     static_assert(COLS % 32 == 0, "columns per thread must be whole TMEM load chunks");
     static_assert(BN % 128 == 0 && BN <= 256, "BN must be 128 or 256");
     static_assert(B_ROWS % B_BOX == 0, "B rows must be whole boxes");
@@ -130,11 +137,76 @@ __device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int
     tn = r / gsize;
 }
 
+// One tile of the output as one CTA sees it.
+struct Tile {
+    int arow;      // first row of A (of sa, and of D but for a grouped wgrad)
+    int drow;      // first row of D
+    int tn;        // column tile
+    int expert;    // grouped: which weight or output, else 0
+    int kb0, kbs;  // reduction blocks kb0 .. kb0 + kbs - 1
+    bool live;     // false: the odd half of a pair past the expert's last block
+};
+
+// Grouped GEMM: expert e owns the 128-row blocks first[e] .. first[e + 1] - 1 of the
+// tokens.  fprop and dgrad cut these into row tiles of CG blocks, tiles[e] of them before
+// expert e's.  Built once per CTA from the caller's table, whose entries are clamped to
+// the blocks there are and made non-decreasing, so that no value in it can lead outside
+// the operands.
+struct GroupTable {
+    int *first, *tiles;  // [E + 1], shared memory
+
+    // One warp.
+    __device__ __forceinline__ void build(const int *seg, int E, int blocks, int cg, int lane) const
+    {
+        int high = 0, before = 0;
+        for (int e0 = 0; e0 <= E; e0 += 32) {
+            const int e = e0 + lane;
+            int v = e <= E ? min(max(seg[e], 0), blocks) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, v, o);
+                v = lane >= o ? max(v, up) : v;
+            }
+            v = max(v, high);
+            int prev = __shfl_up_sync(0xffffffffu, v, 1);
+            if (lane == 0)
+                prev = e0 ? high : v;
+            int n = (v - prev + cg - 1) / cg;  // row tiles of expert e - 1
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, n, o);
+                n += lane >= o ? up : 0;
+            }
+            if (e <= E) {
+                first[e] = v;
+                tiles[e] = before + n;
+            }
+            high = __shfl_sync(0xffffffffu, v, 31);
+            before += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+
+    // The expert whose row tiles include tile tm (tm < tiles[E]).
+    __device__ __forceinline__ int expert_of(int tm, int E) const
+    {
+        int lo = 0, hi = E;  // tiles[lo] <= tm < tiles[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tiles[mid] <= tm)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    }
+};
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmD, const float *__restrict__ sa, const float *__restrict__ sb,
-                void *__restrict__ Dv, int M, int N, int K, int tiles_m, int KB)
+                void *__restrict__ Dv, int M, int N, int K, int tiles_m, int KB,
+                const int *__restrict__ seg, int E)
 {
     constexpr int BN = Cfg::BN, MODE = Cfg::MODE, STAGES = Cfg::STAGES, CG = Cfg::CG;
     constexpr int COLS = Cfg::COLS, EPI_WARPS = Cfg::EPI_WARPS;
@@ -164,8 +236,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     // ends in a partial tile / reduction block: TMA reads zeros past the end of A and
     // B and clips the stores; the scale loader and the direct stores guard the rest.
     const int tiles_n = N / BN;  // tiles_m and KB (ceil divisions) come from the host
-    const int num_tiles = tiles_m * tiles_n;
-
+    int num_tiles = tiles_m * tiles_n;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -197,6 +268,45 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     tc_fence_after();
     pdl_wait();               // inputs written by the previous kernel are visible
     pdl_launch_dependents();  // the next kernel may start its launch and prologue
+    const GroupTable groups = {reinterpret_cast<int *>(smem + Cfg::TABLE_OFF),
+                               reinterpret_cast<int *>(smem + Cfg::TABLE_OFF) + MAX_GROUPS + 1};
+    if constexpr (Cfg::GROUPED) {
+        // blocks of tokens there are: rows of A, or (wgrad) its columns
+        if (warp == 2)
+            groups.build(seg, E, MODE == 2 ? KB : M / 128, CG, lane);
+        __syncthreads();
+        num_tiles = MODE == 2 ? E * num_tiles : groups.tiles[E] * tiles_n;
+    }
+    const auto locate = [&](int t) {
+        Tile o;
+        int tm;
+        if constexpr (Cfg::GROUPED && MODE == 2) {
+            const int per = tiles_m * tiles_n;
+            o.expert = t / per;
+            tile_coords(t - o.expert * per, tiles_m, tiles_n, tm, o.tn);
+            o.kb0 = groups.first[o.expert];
+            o.kbs = groups.first[o.expert + 1] - o.kb0;
+            o.arow = tm * Cfg::TILE_M + rank * BM;
+            o.drow = o.expert * M + o.arow;
+            o.live = true;
+        } else if constexpr (Cfg::GROUPED) {
+            tile_coords(t, groups.tiles[E], tiles_n, tm, o.tn);
+            o.expert = groups.expert_of(tm, E);
+            const int block = groups.first[o.expert] + (tm - groups.tiles[o.expert]) * CG + rank;
+            o.kb0 = 0;
+            o.kbs = KB;
+            o.arow = o.drow = block * BM;
+            o.live = block < groups.first[o.expert + 1];
+        } else {
+            tile_coords(t, tiles_m, tiles_n, tm, o.tn);
+            o.expert = 0;
+            o.kb0 = 0;
+            o.kbs = KB;
+            o.arow = o.drow = tm * Cfg::TILE_M + rank * BM;
+            o.live = true;
+        }
+        return o;
+    };
     const uint32_t tmem_base = *tmem_slot;
     // cluster-window addresses of the even CTA's barriers
     const uint32_t full_lead = (CG == 2) ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
@@ -209,11 +319,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int stage = 0;
             uint32_t phase = 0;
             for (int t = unit; t < num_tiles && !*abort_flag; t += units) {
-                int tm, tn;
-                tile_coords(t, tiles_m, tiles_n, tm, tn);
-                const int arow = tm * Cfg::TILE_M + rank * BM;
-                const int bcol = tn * BN + rank * Cfg::B_ROWS;
-                for (int kb = 0; kb < KB; ++kb) {
+                const Tile o = locate(t);
+                const int arow = o.arow;
+                const int bcol = o.tn * BN + rank * Cfg::B_ROWS + (MODE == 0 ? o.expert * N : 0);
+                const int bk0 = MODE == 1 ? o.expert * K : 0;  // first row of W[K][N]
+                for (int kb = o.kb0; kb < o.kb0 + o.kbs; ++kb) {
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, &g_device_error,
                                            ERR_PRODUCER, WAIT_LIMIT_NS))
                         goto role_done;
@@ -227,7 +337,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                             for (int j = 0; j < Cfg::B_ROWS / Cfg::B_BOX; ++j)
                                 tma_load_2d(sB + j * Cfg::B_BOX * BK, &tmB, &full[stage],
-                                            bcol + j * Cfg::B_BOX, kb * BK);
+                                            bcol + j * Cfg::B_BOX, bk0 + kb * BK);
                         } else {
                             tma_load_2d(sB, &tmB, &full[stage], kb * BK, bcol);
                         }
@@ -241,7 +351,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                             for (int j = 0; j < Cfg::B_ROWS / Cfg::B_BOX; ++j)
                                 tma_load_2d_pair(sB + j * Cfg::B_BOX * BK, &tmB, fb,
-                                                 bcol + j * Cfg::B_BOX, kb * BK);
+                                                 bcol + j * Cfg::B_BOX, bk0 + kb * BK);
                         } else {
                             tma_load_2d_pair(sB, &tmB, fb, kb * BK, bcol);
                         }
@@ -258,7 +368,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 0;
             for (int t = unit; t < num_tiles && !*abort_flag; t += units) {
-                for (int kb = 0; kb < KB; ++kb) {
+                const int kbs = (Cfg::GROUPED && MODE == 2) ? locate(t).kbs : KB;
+                for (int kb = 0; kb < kbs; ++kb) {
                     if (!mbar_spin_bounded(&full[stage], phase, abort_flag, &g_device_error,
                                            ERR_MMA_FULL, WAIT_LIMIT_NS))
                         goto role_done;
@@ -313,11 +424,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             // never waits for global memory and runs up to SRING iterations ahead.
             int j = 0;
             for (int t = unit; t < num_tiles && !*abort_flag; t += units) {
-                int tm, tn;
-                tile_coords(t, tiles_m, tiles_n, tm, tn);
-                const float *sa_tile = sa + tm * Cfg::TILE_M + rank * BM;
+                const Tile o = locate(t);
+                const int tn = o.tn;
+                const float *sa_tile = sa + o.arow;
+                // fprop, dgrad: the expert's weight scales
+                const float *sb_e = sb + size_t(o.expert) * size_t(MODE == 2 ? 0 : N / 128) * KB;
                 const int nb0 = (tn * BN) / 128;
-                for (int kb = 0; kb < KB; ++kb, ++j) {
+                for (int kb = o.kb0; kb < o.kb0 + o.kbs; ++kb, ++j) {
                     const int r = j % Cfg::SRING;
                     const uint32_t ph = uint32_t(j / Cfg::SRING) & 1u;
                     const bool ok = mbar_wait_bounded(&sempty[r], ph ^ 1u, abort_flag,
@@ -328,17 +441,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (MODE == 2) {  // the CTA's 128 row scales (M is a feature count)
                         cp_async_16(slot + 4 * lane, sa_tile + size_t(kb) * M + 4 * lane);
                     } else {  // M counts tokens: rows past M (a partial tile) read as zeros
-                        const int row = tm * Cfg::TILE_M + rank * BM + 4 * lane;
+                        const int row = o.arow + 4 * lane;
                         cp_async_16_zfill(slot + 4 * lane,
                                           row < M ? sa_tile + size_t(kb) * M + 4 * lane : sa,
                                           row < M);
                     }
                     if (MODE == 0) {
                         if (lane < BN / 128)
-                            cp_async_4(slot + BM + lane, sb + size_t(nb0 + lane) * KB + kb);
+                            cp_async_4(slot + BM + lane, sb_e + size_t(nb0 + lane) * KB + kb);
                     } else if (MODE == 1) {
                         if (lane < BN / 128)
-                            cp_async_4(slot + BM + lane, sb + size_t(kb) * (N / 128) + nb0 + lane);
+                            cp_async_4(slot + BM + lane, sb_e + size_t(kb) * (N / 128) + nb0 + lane);
                     } else if (Cfg::WG16) {
                         // Column scales in the order the 16x256b promotion reads them:
                         // column 128 h + 64 cc + 8 j + 2 t0 + e goes to slot position
@@ -368,8 +481,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int ew = warp - Cfg::EPI_WARP0;
         const int quarter = warp & 3;           // TMEM lanes this warp may access
         const int col0 = (ew >> 2) * COLS;      // columns of the tile this thread owns
-        const int row_in_tile = rank * BM + quarter * 32 + lane;
-
         const int row_local = quarter * 32 + lane;  // the thread's row among the CTA's 128
 
         float2 acc[COLS / 2];
@@ -377,13 +488,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (int i = 0; i < COLS / 2; ++i)
             acc[i] = make_float2(0.f, 0.f);
 
-        const int my_tiles = (num_tiles - unit + units - 1) / units;
-        const int total_iters = my_tiles > 0 ? my_tiles * KB : 0;
-
-        int buf = 0, kb = 0, t = unit, tm = 0, tn = 0;
+        int buf = 0, kb = 0, t = unit, j = 0;
         uint32_t tphase = 0;
-        tile_coords(t, tiles_m, tiles_n, tm, tn);
-        for (int j = 0; j < total_iters; ++j) {
+        Tile o = {};
+        if (t < num_tiles)
+            o = locate(t);
+        while (t < num_tiles) {
+            // (an expert without tokens has no blocks: its wgrad tile is stored as zeros)
+            if (!(Cfg::GROUPED && MODE == 2) || o.kbs > 0) {
             const int r = j % Cfg::SRING;
             const bool sready = mbar_wait_bounded(&sfull[r], uint32_t(j / Cfg::SRING) & 1u,
                                                   abort_flag, &g_device_error, ERR_SCALES,
@@ -513,15 +625,25 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sempty[r]);  // this warp is done with the slot's scales
-            if (++kb == KB) {
+            ++kb;
+            ++j;
+            if (++buf == Cfg::NBUF) {
+                buf = 0;
+                tphase ^= 1u;
+            }
+            }
+            if (kb == o.kbs) {
+                const int tn = o.tn;
                 if constexpr (Cfg::OUT32 && Cfg::TMA_STORE) {
                     // FP32 tile -> swizzled staging (32 rows x 64 columns per pass, two
                     // 32x32 boxes) -> bulk tensor reduce-add into the FP32 output.
                     uint8_t *stg = sout + ew * Cfg::STAGE_OUT_WARP;
                     const int t0 = lane & 3, t1 = lane >> 2;
-                    const int r0 = tm * Cfg::TILE_M + rank * BM + quarter * 32;
+                    const int r0 = o.drow + quarter * 32;
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
+                        if (Cfg::GROUPED && o.kbs == 0)
+                            break;  // nothing to add
                         if (lane == 0)
                             bulk_wait_read0();
                         __syncwarp();
@@ -547,13 +669,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 } else if constexpr (Cfg::OUT32) {
                     // Vector atomic adds (red.global.add.v4.f32): calls that overlap on the
                     // same FP32 buffer only reorder their additions, as on the pair path.
-                    float *dst = D32 + size_t(tm * Cfg::TILE_M + row_in_tile) * size_t(N) +
-                                 size_t(tn * BN + col0);
+                    float *dst = D32 + size_t(o.drow + row_local) * size_t(N) + size_t(tn * BN + col0);
 #pragma unroll
                     for (int c = 0; c < COLS / 4; ++c)
-                        atomicAdd(reinterpret_cast<float4 *>(dst + 4 * c),
+                        if (!Cfg::GROUPED || o.kbs > 0)
+                            atomicAdd(reinterpret_cast<float4 *>(dst + 4 * c),
                                   make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
                                               acc[2 * c + 1].y));
+                } else if (Cfg::GROUPED && !o.live) {
+                    // the next expert's rows, or none: another tile's to store
                 } else if (Cfg::TMA_STORE) {
                     // BF16 tile -> swizzled staging -> two bulk tensor stores per warp.
                     uint8_t *stg = sout + ew * Cfg::STAGE_OUT_WARP;
@@ -597,16 +721,16 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        const int r0 = tm * Cfg::TILE_M + rank * BM + quarter * 32;
+                        const int r0 = o.drow + quarter * 32;
 #pragma unroll
                         for (int box = 0; box < COLS / 64; ++box)
                             tma_store_2d(&tmD, stg + box * 4096, tn * BN + col0 + box * 64, r0);
                         bulk_commit();
                     }
                 } else {
-                    __nv_bfloat16 *dst = D + size_t(tm * Cfg::TILE_M + row_in_tile) * size_t(N) +
+                    __nv_bfloat16 *dst = D + size_t(o.drow + row_local) * size_t(N) +
                                          size_t(tn * BN + col0);
-                    if (tm * Cfg::TILE_M + row_in_tile < M) {  // rows past M: not stored
+                    if (MODE == 2 || o.drow + row_local < M) {  // rows past M: not stored
 #pragma unroll
                         for (int c = 0; c < COLS / 8; ++c) {
                             uint4 o;
@@ -628,11 +752,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 kb = 0;
                 t += units;
                 if (t < num_tiles)
-                    tile_coords(t, tiles_m, tiles_n, tm, tn);
-            }
-            if (++buf == Cfg::NBUF) {
-                buf = 0;
-                tphase ^= 1u;
+                    o = locate(t);
             }
         }
         if (Cfg::TMA_STORE && lane == 0)
@@ -731,9 +851,11 @@ static bool make_map_f32_out(CUtensorMap *map, void *base, uint64_t rows, uint64
     return r == CUDA_SUCCESS;
 }
 
+// seg and E: the experts' blocks of a grouped GEMM (E = 1 and no table otherwise).
 template <class Cfg>
 static cudaError_t run(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb,
-                       void *d, int64_t M, int64_t N, int64_t K, cudaStream_t stream, int num_sms)
+                       void *d, int64_t M, int64_t N, int64_t K, cudaStream_t stream, int num_sms,
+                       const int32_t *seg = nullptr, int E = 1)
 {
     auto kern = fp8_gemm_kernel<Cfg>;
     // Per-device launch facts, worked out on the first launch of this configuration on
@@ -783,19 +905,24 @@ static cudaError_t run(const uint8_t *a, const float *sa, const uint8_t *b, cons
         return cudaErrorInvalidValue;
     bool ok;
     if (Cfg::MODE == 1)
-        ok = make_map_u8(&tb, b, uint64_t(K), uint64_t(N), BK, Cfg::B_BOX,  // W[K][N]
+        ok = make_map_u8(&tb, b, uint64_t(E) * K, uint64_t(N), BK, Cfg::B_BOX,  // W[K][N]
                          Cfg::B_BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     else
-        ok = make_map_u8(&tb, b, uint64_t(N), uint64_t(K), Cfg::B_ROWS, BK);
+        ok = make_map_u8(&tb, b, uint64_t(Cfg::MODE == 0 ? E : 1) * N, uint64_t(K), Cfg::B_ROWS, BK);
+    const uint64_t d_rows = uint64_t(Cfg::MODE == 2 ? E : 1) * M;
     if (!ok)
         return cudaErrorInvalidValue;
     CUtensorMap td;
     std::memset(&td, 0, sizeof td);
-    if (Cfg::TMA_STORE && !Cfg::OUT32 && !make_map_bf16_out(&td, d, uint64_t(M), uint64_t(N)))
+    if (Cfg::TMA_STORE && !Cfg::OUT32 && !make_map_bf16_out(&td, d, d_rows, uint64_t(N)))
         return cudaErrorInvalidValue;
-    if (Cfg::TMA_STORE && Cfg::OUT32 && !make_map_f32_out(&td, d, uint64_t(M), uint64_t(N)))
+    if (Cfg::TMA_STORE && Cfg::OUT32 && !make_map_f32_out(&td, d, d_rows, uint64_t(N)))
         return cudaErrorInvalidValue;
-    const int64_t tiles = ((M + Cfg::TILE_M - 1) / Cfg::TILE_M) * (N / Cfg::BN);
+    // grouped: at most this many (each expert may end in half a pair of blocks)
+    const int64_t tiles = (Cfg::MODE == 2 ? E * (M / Cfg::TILE_M + (M % Cfg::TILE_M != 0))
+                           : Cfg::GROUPED && Cfg::CG == 2 ? (M / BM + E) / 2
+                                          : (M + Cfg::TILE_M - 1) / Cfg::TILE_M) *
+                          (N / Cfg::BN);
     void *dp = d;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
@@ -817,7 +944,8 @@ static cudaError_t run(const uint8_t *a, const float *sa, const uint8_t *b, cons
         cfg.gridDim = dim3(unsigned(2 * clusters));
     }
     e = cudaLaunchKernelEx(&cfg, kern, ta, tb, td, sa, sb, dp, int(M), int(N), int(K),
-                           int((M + Cfg::TILE_M - 1) / Cfg::TILE_M), int((K + BK - 1) / BK));
+                           int((M + Cfg::TILE_M - 1) / Cfg::TILE_M), int((K + BK - 1) / BK),
+                           seg, E);
     if (e != cudaSuccess)
         return e;
     return cudaGetLastError();
@@ -872,6 +1000,43 @@ cudaError_t launch_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uin
         return run<GemmCfg<256, 2, 4, 2, true>>(a, sa, b, sb, d32, M, N, K, stream, num_sms);
     return wide ? run<GemmCfg<256, 2, 4, 1, true>>(a, sa, b, sb, d32, M, N, K, stream, num_sms)
                 : run<GemmCfg<128, 2, 6, 1, true>>(a, sa, b, sb, d32, M, N, K, stream, num_sms);
+}
+
+// Grouped GEMM: how many rows each expert has is known to the GPU alone, so the choice
+// goes by the sizes of the whole.
+template <int MODE>
+static cudaError_t run_grouped(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb,
+                               void *d, const int32_t *seg, int E, int64_t M, int64_t N, int64_t K,
+                               cudaStream_t stream, int num_sms)
+{
+    const int64_t row_tiles = MODE == 2 ? E * (M / 128) : M / 128;
+    const bool wide = (N % 256) == 0 && row_tiles * (N / 256) * 2 >= num_sms;
+    return wide ? run<GemmCfg<256, MODE, 4, 1, false, true>>(a, sa, b, sb, d, M, N, K, stream,
+                                                             num_sms, seg, E)
+                : run<GemmCfg<128, MODE, 6, 1, false, true>>(a, sa, b, sb, d, M, N, K, stream,
+                                                             num_sms, seg, E);
+}
+
+cudaError_t launch_gemm_grouped(int mode, const uint8_t *a, const float *sa, const uint8_t *b,
+                                const float *sb, void *d, const int32_t *seg, int E, int64_t M,
+                                int64_t N, int64_t K, cudaStream_t stream, int num_sms)
+{
+    switch (mode) {
+    case 0: return run_grouped<0>(a, sa, b, sb, d, seg, E, M, N, K, stream, num_sms);
+    case 1: return run_grouped<1>(a, sa, b, sb, d, seg, E, M, N, K, stream, num_sms);
+    default: return run_grouped<2>(a, sa, b, sb, d, seg, E, M, N, K, stream, num_sms);
+    }
+}
+
+cudaError_t launch_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b,
+                                            const float *sb, float *d32, const int32_t *seg, int E,
+                                            int64_t M, int64_t N, int64_t K, cudaStream_t stream,
+                                            int num_sms)
+{
+    return (N % 256) == 0 ? run<GemmCfg<256, 2, 4, 1, true, true>>(a, sa, b, sb, d32, M, N, K, stream,
+                                                                   num_sms, seg, E)
+                          : run<GemmCfg<128, 2, 6, 1, true, true>>(a, sa, b, sb, d32, M, N, K, stream,
+                                                                   num_sms, seg, E);
 }
 
 // Self-test of the bounded-wait path: one warp waits, with the same bounded wait the

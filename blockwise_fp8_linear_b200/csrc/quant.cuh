@@ -34,6 +34,16 @@ cudaError_t launch_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uin
                                     const float *sb, float *d32, int64_t M, int64_t N, int64_t K,
                                     cudaStream_t stream, int num_sms);
 
+// Grouped GEMMs: expert e owns the 128-token blocks seg[e] .. seg[e + 1] - 1; b holds E
+// weights (wgrad: d holds E outputs).
+cudaError_t launch_gemm_grouped(int mode, const uint8_t *a, const float *sa, const uint8_t *b,
+                                const float *sb, void *d, const int32_t *seg, int E, int64_t M,
+                                int64_t N, int64_t K, cudaStream_t stream, int num_sms);
+cudaError_t launch_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b,
+                                            const float *sb, float *d32, const int32_t *seg, int E,
+                                            int64_t M, int64_t N, int64_t K, cudaStream_t stream,
+                                            int num_sms);
+
 // GEMM with power-of-two (E8M0) scale codes (uint8, the layouts of the FP32 scales),
 // promoted inside the block-scaled MMA.  Arguments already validated.
 cudaError_t launch_gemm_mx(int mode, const uint8_t *a, const uint8_t *sa, const uint8_t *b,

@@ -34,7 +34,8 @@
  *                the tokens present (the result of zero-padding the tokens to a
  *                multiple of 128, restricted to the tokens present), so token-wise
  *                scale arrays have ceil(tokens/128) rows.  The E8M0 entry points
- *                keep whole groups.
+ *                keep whole groups.  The few-token and mixture-of-experts calls state
+ *                their own limits on tokens, experts and choices.
  *   Alignment    Every pointer must be 16-byte aligned (else FP8BW_EALIGN).
  *   Streams      `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
  *                enqueued asynchronously; no call but fp8bw_last_device_error
@@ -77,6 +78,9 @@ typedef enum {
 typedef enum { FP8BW_FPROP = 0, FP8BW_DGRAD = 1, FP8BW_WGRAD = 2 } fp8bw_mode;
 
 #define FP8BW_MAX_DIM (1 << 20)
+#define FP8BW_FEW_TOKENS 64    /* most tokens of fp8_linear_few and fp8_moe_few */
+#define FP8BW_MAX_EXPERTS 1024 /* most experts of a mixture-of-experts call */
+#define FP8BW_MAX_CHOICES 32   /* most experts that one token may choose */
 
 /*
  * fp8_quant_act -- 1x128 groups along the reduction dimension (section 3.2: the
@@ -212,6 +216,113 @@ int fp8_quant_weight_e8m0(const void *w_bf16, int64_t N, int64_t K, uint8_t *q,
 int fp8_gemm_blockwise_e8m0(int mode, const uint8_t *a, const uint8_t *sa_e8m0,
                             const uint8_t *b, const uint8_t *sb_e8m0, void *d_bf16, int64_t M,
                             int64_t N, int64_t K, void *stream);
+
+/*
+ * ---- Few tokens: the linear of a decode step ----
+ *
+ * fp8_linear_few -- Y[M][N] = X . W^T for M = 1 .. FP8BW_FEW_TOKENS tokens (any such
+ * number), in one launch: X is quantized inside the kernel exactly as fp8_quant_act
+ * would (the same codes and scales), then multiplied as by fp8_gemm_blockwise(FPROP).
+ *   x [M][K] BF16     qw [N][K], sw [N/128][K/128] from fp8_quant_weight
+ *   y [M][N] BF16, written, never read
+ * M out of range returns FP8BW_ESHAPE.
+ */
+int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void *y_bf16,
+                   int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * ---- Mixture of experts ----
+ * T tokens, E experts (1 .. FP8BW_MAX_EXPERTS), k choices per token (1 .. min(E,
+ * FP8BW_MAX_CHOICES)); sizes outside these, or T outside 1 .. FP8BW_MAX_DIM, return
+ * FP8BW_ESHAPE.  A choice is named by the pair index t * k + j.  An id outside [0, E)
+ * marks a choice that is left out.
+ *
+ * fp8_moe_route -- softmax router.  ids[t][0..k-1] are the experts of the k largest
+ * logits of row t, largest first, ties to the lowest expert; weights[t][j] is the
+ * softmax of the logits, taken over the chosen experts (renorm != 0) or over all.
+ *   logits [T][E] FP32 or (bf16 != 0) BF16      weights [T][k] FP32      ids [T][k] int32
+ * A logit of -infinity or NaN is never chosen and has probability zero; a row with
+ * fewer than k others gets id -1 and weight 0 in the places left.  +infinity counts as
+ * the largest finite FP32 value.
+ */
+int fp8_moe_route(const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
+                  float *weights, int32_t *ids, void *stream);
+
+/*
+ * fp8_moe_route_bwd -- gradient of the logits: with g_j = weights_j dweights_j and
+ * G = sum_j g_j,  dlogits = [chosen] g - p G, where p is the softmax over the chosen
+ * experts (renorm; zero elsewhere) or over all.  weights, ids and logits are those of
+ * the forward call; dlogits [T][E] has the type of logits and is written whole.
+ */
+int fp8_moe_route_bwd(const float *dweights, const float *weights, const int32_t *ids,
+                      const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
+                      void *dlogits, void *stream);
+
+/*
+ * fp8_moe_plan -- lays the pairs out by expert for the grouped GEMMs: expert e gets the
+ * blocks of 128 rows seg[e] .. seg[e + 1] - 1 (seg[0] = 0), as many as its pairs need,
+ * and its pairs stand there in pair order.
+ *   ids [T][k]      seg [E + 1] int32
+ *   row [T][k] int32: the row of each pair, -1 for one that is left out
+ *   src [rows] int32: the pair of each row, -1 for a row that no pair takes;
+ *       rows = fp8_moe_plan_rows(T, E, k) holds any split of the pairs
+ *   workspace: fp8_moe_plan_workspace(T, E, k) bytes, not shared with a call that may
+ *       run at the same time
+ * FP8BW_ESHAPE also if rows exceeds FP8BW_MAX_DIM.  The two size functions return 0 for
+ * sizes that the call rejects.
+ */
+int64_t fp8_moe_plan_rows(int64_t T, int64_t E, int64_t k);
+int64_t fp8_moe_plan_workspace(int64_t T, int64_t E, int64_t k);
+int fp8_moe_plan(const int32_t *ids, int64_t T, int64_t E, int64_t k, int32_t *seg, int32_t *row,
+                 int32_t *src, void *workspace, void *stream);
+
+/*
+ * fp8_gemm_grouped -- fp8_gemm_blockwise with one weight per expert.  The tokens (M of
+ * FPROP and DGRAD, K of WGRAD; here a multiple of 128) are laid out by expert as above,
+ * with zeros in the rows that no pair takes (so that they do not enter WGRAD):
+ *   FPROP  a = Qx [M][K], sa = [K/128][M], b = Qw [E][N][K], sb = [E][N/128][K/128],
+ *          d [M][N]
+ *   DGRAD  a = Qdy [M][K], sa = [K/128][M], b = Qw [E][K][N], sb = [E][K/128][N/128],
+ *          d [M][N]
+ *   WGRAD  a = Qdy^T [M][K], sa = [K/128][M], b = Qx^T [N][K], sb = [K/128][N],
+ *          d [E][M][N]: one weight gradient per expert, zero for one without blocks
+ *   seg [E + 1] int32 on the device; entries are clamped to [0, blocks] and to their
+ *   predecessors.  Rows of d in blocks that no expert owns are left as they were.
+ * E times each of M (WGRAD), N and K (FPROP, DGRAD) must not exceed 2^30.
+ */
+int fp8_gemm_grouped(int mode, const uint8_t *a, const float *sa, const uint8_t *b,
+                     const float *sb, const int32_t *seg, int64_t E, void *d_bf16, int64_t M,
+                     int64_t N, int64_t K, void *stream);
+
+/* fp8_gemm_grouped_wgrad_acc32 -- the grouped WGRAD added into FP32 main gradients:
+ *   dw32 [E][M][N] FP32, read and written; an expert without blocks is not touched. */
+int fp8_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b,
+                                 const float *sb, const int32_t *seg, int64_t E, float *dw32,
+                                 int64_t M, int64_t N, int64_t K, void *stream);
+
+/*
+ * fp8_moe_few -- all experts of a SwiGLU layer for T = 1 .. FP8BW_FEW_TOKENS tokens, in
+ * two launches: for each token t and chosen expert e
+ *   g, u = X[t] . W1_e^T (gate rows first, then up rows),  h = g / (1 + exp(-g)) * u,
+ *   y[t] = sum_j weights[t][j] (h . W2_e^T)
+ * X and h are quantized per 1x128 group (h from FP32, scale amax/448), each expert's
+ * weights are read once, sums are FP32 and y is rounded to BF16 once.
+ *   x [T][H] BF16
+ *   w1 [E][2I][H], s1 [E][2I/128][H/128]     w2 [E][H][I], s2 [E][H/128][I/128]
+ *     (fp8_quant_weight of the matrices stacked by expert)
+ *   ids, weights [T][k] as from fp8_moe_route; a token that names an expert twice gives
+ *     it the sum of the two weights; one whose choices are all left out gets y = 0
+ *   y [T][H] BF16, written, never read
+ *   workspace: fp8_moe_few_workspace(T, k, H, I) bytes (0 for sizes that the call
+ *     rejects); calls that may run at the same time need one each, as do two captured
+ *     graphs that may
+ * H and I multiples of 128; E * 2I and E * H at most 2^30.
+ */
+int64_t fp8_moe_few_workspace(int64_t T, int64_t k, int64_t H, int64_t I);
+int fp8_moe_few(const void *x_bf16, const uint8_t *w1, const float *s1, const uint8_t *w2,
+                const float *s2, const int32_t *ids, const float *weights, void *y_bf16,
+                int64_t T, int64_t E, int64_t k, int64_t H, int64_t I, void *workspace,
+                void *stream);
 
 /* Human-readable name of a status code (static string). */
 const char *fp8bw_status_string(int status);

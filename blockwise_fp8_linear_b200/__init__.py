@@ -27,7 +27,7 @@ __all__ = [
     "fp8bw_selftest_wait_timeout",
     "linear_fprop", "linear_dgrad", "linear_wgrad",
     "FEW_TOKENS", "MAX_EXPERTS", "MAX_CHOICES",
-    "fp8_linear_few", "fp8_moe_route", "fp8_moe_route_bwd", "fp8_moe_plan_rows", "fp8_moe_plan",
+    "fp8_linear_few", "fp8_linear_few_workspace", "fp8_moe_route", "fp8_moe_route_bwd", "fp8_moe_plan_rows", "fp8_moe_plan",
     "fp8_gemm_grouped", "fp8_gemm_grouped_wgrad_acc32", "fp8_moe_few", "fp8_moe_few_workspace",
 ]
 
@@ -66,7 +66,9 @@ def lib():
         L.fp8_quant_act_dual_e8m0.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp]
         L.fp8_quant_weight_e8m0.argtypes = [vp, i64, i64, vp, vp, vp, vp]
         L.fp8_gemm_blockwise_e8m0.argtypes = [i32, vp, vp, vp, vp, vp, i64, i64, i64, vp]
-        L.fp8_linear_few.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        L.fp8_linear_few.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp]
+        L.fp8_linear_few_workspace.argtypes = [i64, i64]
+        L.fp8_linear_few_workspace.restype = i64
         L.fp8_moe_route.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
         L.fp8_moe_route_bwd.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, vp]
         L.fp8_moe_plan.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
@@ -107,10 +109,12 @@ def fp8bw_version() -> str:
 
 
 def _stream(stream):
+    """The cudaStream_t of a call: of the given stream, or of the current device's current
+    one (asked for as a plain number: making a Stream object costs more than a launch)."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(status: int, what: str):
@@ -126,11 +130,12 @@ def _validate(items):
     the C call would let a kernel read or write past an allocation, so every mismatch
     raises here (ValueError for shapes and devices, TypeError for kinds)."""
     import torch
-    given = [(t, dt, shp, name) for t, dt, shp, name in items if t is not None]
+    Tensor = torch.Tensor
+    given = [i for i in items if i[0] is not None]
     for t, _, shp, name in given:
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if tuple(t.shape) != tuple(int(d) for d in shp):
+        if t.shape != shp:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shp)}")
     for t, dt, _, name in given:
         if t.dtype != dt:
@@ -139,16 +144,17 @@ def _validate(items):
             raise ValueError(f"{name} must be contiguous")
         if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-    dev = given[0][0].device
+    first = given[0][0].get_device()
     for t, _, _, name in given:
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev} (one device per call)")
-    return dev
+        if t.get_device() != first:
+            raise ValueError(f"{name} is on {t.device}, expected {given[0][0].device} "
+                             "(one device per call)")
+    return given[0][0].device
 
 
 def _alloc(t, shape, dtype, device):
     import torch
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+    return torch.empty(*shape, dtype=dtype, device=device) if t is None else t
 
 
 def _dims(M, N=None, K=None):
@@ -159,10 +165,25 @@ def _dims(M, N=None, K=None):
             raise ValueError(f"size {d} is not a positive multiple of 128")
 
 
+class _Current:
+    """The context of a call whose device is current already."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_current = _Current()
+
+
 def _on(device):
     """Context that makes `device` current, so the call's stream and the current device
     match its buffers (the ABI rejects buffers of another device)."""
     import torch
+    if torch.cuda.current_device() == device.index:
+        return _current
     return torch.cuda.device(device)
 
 
@@ -448,9 +469,11 @@ def linear_wgrad(dy, x, stream=None):
 
 # -- few tokens: the linear of a decode step --------------------------------------
 
-def fp8_linear_few(x, qw, sw, out=None, stream=None):
+def fp8_linear_few(x, qw, sw, out=None, workspace=None, stream=None):
     """Y[M][N] bf16 = X W^T for X[M][K] bf16 with 1 <= M <= FEW_TOKENS tokens and a weight
-    quantized by fp8_quant_weight; X is quantized inside the call as by fp8_quant_act."""
+    quantized by fp8_quant_weight; X is quantized inside the call as by fp8_quant_act.
+    workspace: uint8, fp8_linear_few_workspace(M, K) bytes or more, one for each call (or
+    captured graph) that may run at the same time."""
     import torch
     M, K = _few_rows(x, "x")
     if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
@@ -460,11 +483,23 @@ def fp8_linear_few(x, qw, sw, out=None, stream=None):
     dev = _validate([(x, torch.bfloat16, (M, K), "x"), (qw, torch.uint8, (N, K), "qw"),
                      (sw, torch.float32, (N // 128, K // 128), "sw"),
                      (out, torch.bfloat16, (M, N), "out")])
+    need = lib().fp8_linear_few_workspace(M, K)
     with _on(dev):
         out = _alloc(out, (M, N), torch.bfloat16, dev)
+        if need:
+            workspace = _workspace(workspace, need, dev, stream)
         _check(lib().fp8_linear_few(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), out.data_ptr(),
-                                    M, N, K, _stream(stream)), "fp8_linear_few")
+                                    M, N, K, workspace.data_ptr() if need else None,
+                                    _stream(stream)), "fp8_linear_few")
     return out
+
+
+def fp8_linear_few_workspace(M: int, K: int) -> int:
+    """Bytes of workspace that fp8_linear_few needs (0 for the smallest token counts)."""
+    if not 1 <= int(M) <= FEW_TOKENS:
+        raise ValueError(f"{M} tokens, expected 1 to {FEW_TOKENS}")
+    _dims(K)
+    return int(lib().fp8_linear_few_workspace(int(M), int(K)))
 
 
 def _few_rows(x, name):

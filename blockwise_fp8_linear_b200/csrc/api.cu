@@ -309,20 +309,28 @@ int fp8_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_t *b, co
 
 // ---- few tokens and mixture of experts ----
 
+int64_t fp8_linear_few_workspace(int64_t M, int64_t K)
+{
+    return M > 0 && M <= FP8BW_FEW_TOKENS && dim_ok(K)
+               ? int64_t(fp8bw::linear_few_workspace(int(M), K)) : 0;
+}
+
 int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void *y_bf16, int64_t M,
-                   int64_t N, int64_t K, void *stream)
+                   int64_t N, int64_t K, void *workspace, void *stream)
 {
     if (!none_null({x_bf16, qw, sw, y_bf16}))
         return FP8BW_EINVAL;
     if (M <= 0 || M > FP8BW_FEW_TOKENS || !dim_ok(N) || !dim_ok(K))
         return FP8BW_ESHAPE;
-    if (!all_aligned16({x_bf16, qw, sw, y_bf16}))
+    if (!workspace && fp8_linear_few_workspace(M, K) > 0)
+        return FP8BW_EINVAL;
+    if (!all_aligned16({x_bf16, qw, sw, y_bf16, workspace}))
         return FP8BW_EALIGN;
     int st;
-    const int sms = device_sms({x_bf16, qw, sw, y_bf16}, &st);
+    const int sms = device_sms({x_bf16, qw, sw, y_bf16, workspace}, &st);
     if (sms < 0)
         return st;
-    return from_cuda(fp8bw::launch_linear_few(x_bf16, int(M), qw, sw, y_bf16, N, K,
+    return from_cuda(fp8bw::launch_linear_few(x_bf16, int(M), qw, sw, y_bf16, N, K, workspace,
                                               static_cast<cudaStream_t>(stream), sms));
 }
 

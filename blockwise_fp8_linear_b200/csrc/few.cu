@@ -10,21 +10,26 @@
 // bound by HBM (by latency when the weights are small).  The product is turned over:
 // 128 weight rows are the MMA's M, the tokens its N (16, 32 or 64 columns), so that one
 // tcgen05.mma takes a whole 128 x 32 weight tile and TMA streams weights straight into
-// shared memory without passing through registers.  One CTA takes a tile of 128
-// weight rows (up: 128 gate rows and the 128 up rows beside them) and one part of the
-// reduction; the CTAs of a cluster split the reduction, so that a small weight still
-// keeps most SMs reading, and join their FP32 sums through distributed shared memory in
-// a fixed order.
+// shared memory without passing through registers.  An item of work is a tile of 128
+// weight rows (up: 128 gate rows and the 128 up rows beside them) for the tokens of one
+// expert.  CTAs, two to an SM, walk the items; the loads run ahead into the next item
+// while one is finished.  Where the items are fewer than the SMs can take, the CTAs of a
+// cluster split the reduction of one item between them and join their FP32 sums through
+// distributed shared memory in a fixed order.
 //
 //   warps 0..3  promotion: partial sums of a 128-block from TMEM (thread = weight row),
 //               times weight scale x token scale, into FP32 sums in registers
-//   warp 4      TMA producer: weight tiles (down: also the codes of h)
+//   warp 4      TMA producer: weight tiles, and the tokens' codes where memory has them
 //   warp 5      MMA issuer
-//   warps 6..   linear, up: quantize the tokens' 1x128 groups of this block into shared
-//               memory (the arithmetic of fp8_quant_act); down: load the scales of h
+//   warps 6..   linear, up: quantize the tokens' 1x128 groups into shared memory (the
+//               arithmetic of fp8_quant_act), one block per warp in turn; otherwise one warp
+//               that loads the scales of the codes
 //
-// An expert's rows: the tokens that chose it, in token order.  Every CTA works them out
-// from the ids, which are at most 2048 numbers.  Every wait is bounded.
+// The rows of the experts are the (token, choice) pairs sorted by expert, in pair order;
+// an item takes up to 32 of one expert's.  Every CTA sorts the ids for itself (they are
+// at most 2048) before its first item.  Columns of the MMA without a token hold whatever
+// the stage held before: columns do not mix, and theirs are not stored.  Every wait is
+// bounded.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -33,6 +38,7 @@
 #include "launch_cache.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
+#include "quant.cuh"
 #include "quant_math.cuh"
 #include "tensor_map.cuh"
 
@@ -43,16 +49,21 @@ constexpr uint64_t FEW_WAIT_NS = 1000000000ull;
 constexpr uint64_t FEW_DRAIN_NS = 20000000ull;
 enum : int { FERR_PRODUCER = 31, FERR_MMA_FULL = 32, FERR_MMA_TEMPTY = 33, FERR_PROMO = 34, FERR_ACT = 35 };
 
-enum : int { FEW_LINEAR = 0, FEW_UP = 1, FEW_DOWN = 2 };
+// FEW_CODES: the linear on codes that fp8_quant_act's kernel has made.
+enum : int { FEW_LINEAR = 0, FEW_UP = 1, FEW_DOWN = 2, FEW_CODES = 3 };
+
+constexpr int FEW_MAX_SPLIT = 8;  // CTAs of a cluster
 
 struct FewArgs {
     const __nv_bfloat16 *x;  // [T][K] (linear, up)
     const float *sw;         // weight block scales [E][N/128][K/128]
     const int32_t *ids;      // [T][k] (up, down)
     const float *weights;    // [T][k] (down)
-    __nv_bfloat16 *y;        // [T][N] (linear, down)
-    uint8_t *hq;             // [T*k][I] codes of h, rows by expert (up writes, down reads)
-    float *hs;               // [I/128][T*k] their scales
+    __nv_bfloat16 *y;        // [T][N] (linear, codes, down)
+    uint8_t *hq;             // [T*k][I] codes of h, rows by expert (up writes)
+    float *hs;               // [I/128][T*k] their scales (up writes)
+    const float *sx;         // [K/128][sx_rows] scales of the codes (down, codes)
+    int sx_rows;
     float *part;             // [T*k][H] products of each pair (down)
     int *count;              // [T][H/128] experts of the token that are done (down)
     int T, k, E;
@@ -63,118 +74,97 @@ struct FewArgs {
 template <int KIND_, int NT_>
 struct FewCfg {
     static constexpr int KIND = KIND_;
+    static constexpr bool EXPERTS = KIND == FEW_UP || KIND == FEW_DOWN;
+    static constexpr bool QUANT = KIND == FEW_LINEAR || KIND == FEW_UP;
     static constexpr int NT = NT_;                      // token columns of the MMA
     static constexpr int RT = KIND == FEW_UP ? 2 : 1;   // 128-row tiles: gate and up, or one
     static constexpr int W_BYTES = RT * 128 * 128;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    // Two CTAs share an SM, so one's prologue and epilogue run under the other's loads;
-    // up with 64 columns keeps 128 sums per thread and has an SM to itself.
-    static constexpr int BLOCKS = RT * NT <= 64 ? 2 : 1;
-    static constexpr int STAGES = 216 / BLOCKS * 1024 / STAGE_BYTES;
-    static constexpr int ACT_WARPS = KIND == FEW_DOWN ? 1 : 4;
+    static constexpr int BLOCKS = 2;                    // CTAs per SM
+    // (up has two, which leaves its promotion warps the registers for their sums)
+    static constexpr int ACT_WARPS = KIND == FEW_LINEAR ? 4 : KIND == FEW_UP ? 2 : 1;
     static constexpr int THREADS = (6 + ACT_WARPS) * 32;
     static constexpr int NBUF = 2;
-    static constexpr int TMEM_COLS = NBUF * RT * NT;    // 32 .. 256, a power of two
-    static constexpr int RED_BYTES = RT * NT * 128 * 4;  // the joined sums reuse the stages
-    static constexpr int XS_OFF = STAGES * STAGE_BYTES;
-    static constexpr int BAR_OFF = XS_OFF + STAGES * NT * 4;
+    static constexpr int TMEM_COLS = NBUF * RT * NT;    // 32 .. 128, a power of two
+    // finished sums of one item, [NT][128]; before the first item, scratch of the plan
+    static constexpr int RED_BYTES = NT * 128 * 4;
+    static constexpr int MAX_PAIRS = !EXPERTS ? 0 : NT == 16 ? 16 * 32 : 64 * 32;
+    static constexpr int MAX_UNITS = !EXPERTS ? 0 : (NT == 16 ? MAX_PAIRS : 1024) + MAX_PAIRS / NT;
+    static constexpr int FIXED = RED_BYTES + MAX_UNITS * 4 + MAX_PAIRS * 2 + 1024 + 512;
+    static constexpr int STAGES = (112 * 1024 - FIXED) / (STAGE_BYTES + NT * 4);
+    static constexpr int RED_OFF = STAGES * STAGE_BYTES;
+    static constexpr int XS_OFF = RED_OFF + RED_BYTES;          // [STAGES][NT] token scales
+    static constexpr int UNIT_OFF = XS_OFF + STAGES * NT * 4;   // [MAX_UNITS] unsigned
+    static constexpr int ORDER_OFF = UNIT_OFF + MAX_UNITS * 4;  // [MAX_PAIRS] 16-bit
+    static constexpr int BAR_OFF = ORDER_OFF + MAX_PAIRS * 2;
     static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 2 * NBUF) * 8 + 16;
-    static_assert(RED_BYTES <= STAGES * STAGE_BYTES, "the joined sums must fit the stages");
+    static_assert(RT * RED_BYTES <= STAGES * STAGE_BYTES, "a cluster's parts take the stages");
+    static_assert(!EXPERTS || MAX_PAIRS * 2 + 1024 * 4 <= RED_BYTES, "the plan's scratch");
     static_assert(TMEM_COLS >= 32 && TMEM_COLS * BLOCKS <= 512, "tensor memory of an SM");
-    // 228 KB per SM, 1 KB of it reserved per CTA; FewPlan is static
-    static_assert((SMEM + 1024 + 512) * BLOCKS <= 228 * 1024, "shared memory of an SM");
+    // 228 KB per SM, 1 KB of it reserved per CTA
+    static_assert((SMEM + 1024 + 64) * BLOCKS <= 228 * 1024, "shared memory of an SM");
 };
 
-// What one CTA of the expert kernels works on: the expert, its rows and where they stand.
-struct FewItem {
-    int expert;  // -1: no such item
-    int rows;
-    int base;    // first row of the expert in the order by (expert, token)
+// Some of one expert's rows, packed into a word: expert, first row (among all experts'),
+// how many.
+struct FewUnit {
+    int expert, base, rows;
+    __device__ __forceinline__ static uint32_t pack(int expert, int base, int rows)
+    {
+        return uint32_t(expert) << 20 | uint32_t(base) << 8 | uint32_t(rows);
+    }
+    __device__ __forceinline__ static FewUnit of(uint32_t w)
+    {
+        return {int(w >> 20), int(w >> 8 & 0xFFFu), int(w & 0xFFu)};
+    }
 };
 
-struct FewPlan {
-    uint32_t hit[32];               // experts that some token chose
-    uint32_t mask[2];               // tokens of this expert
-    int16_t row_pair[kFewMaxTokens];  // pair (token * k + choice) of each row
-    uint8_t row_token[kFewMaxTokens];
-    int expert, base;
-};
-
-// Expert number `slot` among those that some token chose, its tokens in order, and how
-// many (expert, token) rows the experts before it have.  A token that names an expert
-// twice counts once, at its first choice.  All threads of the CTA call it; `id` is
-// scratch in shared memory, one entry per pair.
-__device__ __forceinline__ FewItem few_plan(FewPlan &p, int16_t *id, const int32_t *ids, int T, int k,
-                                            int E, int slot)
+// Counts per expert (n[E], shared) -> where each expert's rows start (in its place) and
+// the units of at most NT rows.  One warp; returns how many units there are.
+template <int NT>
+__device__ __forceinline__ int few_units(int *n, int E, uint32_t *units, int lane)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < 32)
-        p.hit[tid] = 0;
-    if (tid == 0) {
-        p.expert = -1;
-        p.base = 0;
-    }
-    __syncthreads();
-    for (int i = tid; i < T * k; i += blockDim.x) {
-        const int v = ids[i];
-        const bool ok = v >= 0 && v < E;
-        id[i] = int16_t(ok ? v : -1);
-        if (ok)
-            atomicOr(&p.hit[v >> 5], 1u << (v & 31));
-    }
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t word = p.hit[lane];
-        const int n = __popc(word);
-        int before = n;
+    int row0 = 0, unit0 = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        const int c = e < E ? n[e] : 0, u = (c + NT - 1) / NT;
+        int sum = u << 16 | c;  // both sums at once: at most 2048 rows and 1088 units
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, before, o);
-            before += lane >= o ? up : 0;
+            const int up = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= o ? up : 0;
         }
-        before -= n;
-        if (slot >= before && slot < before + n) {
-            for (int i = before; i < slot; ++i)
-                word &= word - 1;
-            p.expert = lane * 32 + __ffs(word) - 1;
+        const int row = row0 + (sum & 0xFFFF) - c, unit = unit0 + (sum >> 16) - u;
+        if (e < E)
+            n[e] = row;
+        for (int i = 0; i < u; ++i)
+            units[unit + i] = FewUnit::pack(e, row + i * NT, min(NT, c - i * NT));
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        row0 += all & 0xFFFF;
+        unit0 += all >> 16;
+    }
+    return unit0;
+}
+
+// Places the pairs: order[row] = pair, in pair order within an expert.  One warp; at[e]
+// is the expert's next row.
+__device__ __forceinline__ void few_order(const int16_t *id, int pairs, int *at, int16_t *order,
+                                          int lane)
+{
+    for (int p0 = 0; p0 < pairs; p0 += 32) {
+        const int e = p0 + lane < pairs ? int(id[p0 + lane]) : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        int row = 0;
+        if (e >= 0) {
+            row = at[e] + __popc(same & ((1u << lane) - 1u));
+            order[row] = int16_t(p0 + lane);
         }
+        __syncwarp();
+        if (e >= 0 && lane == 31 - __clz(same))
+            at[e] = row + 1;
+        __syncwarp();
     }
-    __syncthreads();
-    const int e = p.expert;
-    if (e < 0)
-        return {-1, 0, 0};
-    int earlier = 0;
-    for (int i = tid; i < T * k; i += blockDim.x) {
-        const int v = id[i];
-        if (v >= 0 && v < e) {
-            bool first = true;
-            for (int q = i / k * k; q < i; ++q)
-                first = first && id[q] != v;
-            earlier += first ? 1 : 0;
-        }
-    }
-    earlier = __reduce_add_sync(0xffffffffu, earlier);
-    if (lane == 0 && earlier)
-        atomicAdd(&p.base, earlier);
-    int choice = -1;
-    if (tid < kFewMaxTokens) {
-        if (tid < T)
-            for (int j = k - 1; j >= 0; --j)
-                if (id[tid * k + j] == e)
-                    choice = j;
-        const uint32_t m = __ballot_sync(0xffffffffu, choice >= 0);
-        if (lane == 0)
-            p.mask[warp] = m;
-    }
-    __syncthreads();
-    if (choice >= 0) {
-        const int r = __popc(p.mask[warp] & ((1u << lane) - 1u)) + (warp ? __popc(p.mask[0]) : 0);
-        p.row_token[r] = uint8_t(tid);
-        p.row_pair[r] = int16_t(tid * k + choice);
-    }
-    __syncthreads();
-    return {e, __popc(p.mask[0]) + __popc(p.mask[1]), p.base};
 }
 
 __device__ __forceinline__ uint2 bf16x4(float4 v)
@@ -183,22 +173,125 @@ __device__ __forceinline__ uint2 bf16x4(float4 v)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// This lane's choice of token t (lane j: choice j): its id, -1 where a lower choice names
-// the same expert, and the weight of all choices that name it, summed in their order.
-__device__ __forceinline__ int few_choice(const FewArgs &a, int t, int lane, float &weight)
+__device__ __forceinline__ float swiglu(float g, float u)
 {
-    int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
-    if (id < 0 || id >= a.E)
-        id = -1;
-    const float w = lane < a.k ? a.weights[t * a.k + lane] : 0.0f;
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    weight = 0.0f;
+    return g / (1.0f + expf(-g)) * u;
+}
+
+// Lane j: choice j of token t, -1 where it is left out.
+__device__ __forceinline__ int few_choice(const FewArgs &a, int t, int lane)
+{
+    const int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
+    return id >= 0 && id < a.E ? id : -1;
+}
+
+// One row of an item, finished by one warp: lane l has columns 4 l .. 4 l + 3 of its tile
+// (g, u: of the gate and up rows; otherwise v).
+__device__ __forceinline__ void few_store(const FewArgs &a, int r, int tile, int lane, float4 v)
+{
+    *reinterpret_cast<uint2 *>(a.y + size_t(r) * a.N + tile * 128 + 4 * lane) = bf16x4(v);
+}
+
+__device__ __forceinline__ void few_store_h(const FewArgs &a, int row, int tile, int lane, float4 h)
+{
+    float amax = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // h is kept in FP32 up to its one rounding onto E4M3
+    const float sc = __fdiv_rn(amax, 448.0f);
+    uint32_t codes = 0u;
+    if (sc != 0.0f)
+        codes = cvt_e4m3x2(__fdiv_rn(h.x, sc), __fdiv_rn(h.y, sc)) |
+                (cvt_e4m3x2(__fdiv_rn(h.z, sc), __fdiv_rn(h.w, sc)) << 16);
+    *reinterpret_cast<uint32_t *>(a.hq + size_t(row) * (a.N / 2) + tile * 128 + 4 * lane) = codes;
+    if (lane == 0)
+        a.hs[size_t(tile) * (a.T * a.k) + row] = sc;
+}
+
+// The pair's product goes to memory; the warp that brings a token's last one adds them
+// all, in the order of the choices.
+__device__ __forceinline__ void few_combine(const FewArgs &a, int pair, int tile, int lane, float4 v)
+{
+    const int t = pair / a.k;
+    const size_t col = size_t(tile) * 128 + 4 * lane;
+    const int id = few_choice(a, t, lane);
+    const float weight = lane < a.k ? a.weights[t * a.k + lane] : 0.0f;
+    *reinterpret_cast<float4 *>(a.part + size_t(pair) * a.N + col) = v;
+    const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+    __threadfence();
+    __syncwarp();
+    int done = 0;
+    if (lane == 0)
+        done = atomicAdd(&a.count[t * (a.N / 128) + tile], 1) + 1;
+    done = __shfl_sync(0xffffffffu, done, 0);
+    if (done != __popc(live))
+        return;
+    __threadfence();
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < a.k; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        if ((same >> j) & 1u)
-            weight += wj;
+        const float w = __shfl_sync(0xffffffffu, weight, j);
+        if (!((live >> j) & 1u))
+            continue;
+        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part + size_t(t * a.k + j) * a.N + col));
+        y.x = fmaf(w, p.x, y.x);
+        y.y = fmaf(w, p.y, y.y);
+        y.z = fmaf(w, p.z, y.z);
+        y.w = fmaf(w, p.w, y.w);
     }
-    return (id >= 0 && __ffs(same) - 1 == lane) ? id : -1;
+    few_store(a, t, tile, lane, y);
+}
+
+// Quantizes up to 2 P rows of one 128-block: half-warp h takes rows r0 + 2 q + h, lane
+// `sub` of it 8 neighbouring values (v[q]).  The P chains of maximum, scale and division
+// run side by side.
+template <int P>
+__device__ __forceinline__ void few_quant(const uint4 (&v)[P], int r0, int rows, int lane, uint8_t *sx,
+                                          float *xs)
+{
+    const int sub = lane & 15;
+    uint32_t m2[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+        m2[q] = __vmaxu2(absmax2(v[q].x, v[q].y), absmax2(v[q].z, v[q].w));
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1)
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            m2[q] = __vmaxu2(m2[q], __shfl_xor_sync(0xffffffffu, m2[q], o));
+    float sc[P];
+    bool fast = true;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        sc[q] = scale_of_amax(halves_max_to_float(m2[q]));
+        fast = fast && (m2[q] == 0u || (sc[q] >= 0x1p-90f && sc[q] <= 0x1p90f));
+    }
+    uint2 c[P];
+    if (__all_sync(0xffffffffu, fast)) {
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            c[q] = quant8_fast(v[q], __frcp_rn(m2[q] ? sc[q] : 1.0f), sc[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            c[q] = quant8_ieee(v[q], sc[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        const int r = r0 + 2 * q + (lane >> 4);
+        if (r < rows) {
+            *reinterpret_cast<uint2 *>(sx + r * 128 + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8) =
+                m2[q] ? c[q] : make_uint2(0u, 0u);  // an all-zero group has codes 0
+            if (sub == 0)
+                xs[r] = sc[q];
+        }
+    }
+}
+
+// The 128 threads of the promotion warps.
+__device__ __forceinline__ void promo_sync()
+{
+    asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
 template <class Cfg>
@@ -211,23 +304,28 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *xs = reinterpret_cast<float *>(smem + Cfg::XS_OFF);       // [STAGES][NT] token scales
+    float *red = reinterpret_cast<float *>(smem + Cfg::RED_OFF);
+    float *xs = reinterpret_cast<float *>(smem + Cfg::XS_OFF);
+    uint32_t *units = reinterpret_cast<uint32_t *>(smem + Cfg::UNIT_OFF);
+    int16_t *order = reinterpret_cast<int16_t *>(smem + Cfg::ORDER_OFF);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + NBUF;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + NBUF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    __shared__ FewPlan plan;
+    __shared__ int unit_count;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = int(cluster_ctarank()), split = int(cluster_nctarank());
-    const int tile = int(blockIdx.x) / split;
+    // the plan's scratch: the pairs' ids, and a count per expert
+    int *count = reinterpret_cast<int *>(red);
+    int16_t *id = reinterpret_cast<int16_t *>(red + 1024);
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1 + Cfg::ACT_WARPS);
-            mbar_init(&empty[s], 1 + 4);
+            mbar_init(&full[s], 2);   // the producer's bytes, and the codes or scales
+            mbar_init(&empty[s], 4);  // the promotion warps, when the MMA is done
         }
         for (int b = 0; b < NBUF; ++b) {
             mbar_init(&tfull[b], 1);
@@ -237,18 +335,12 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         fence_mbarrier_init();
         tma_prefetch_desc(&tmW);
     }
+    if (Cfg::EXPERTS)
+        for (int e = tid; e < a.E; e += Cfg::THREADS)
+            count[e] = 0;
     if (warp == 5) {
         tmem_alloc<1>(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish<1>();
-    }
-    if (KIND != FEW_DOWN) {
-        // columns without a token stay zero for good
-        for (int i = tid; i < STAGES * Cfg::X_BYTES / 16; i += Cfg::THREADS) {
-            const int s = i / (Cfg::X_BYTES / 16), o = i % (Cfg::X_BYTES / 16);
-            *reinterpret_cast<uint4 *>(smem + s * Cfg::STAGE_BYTES + Cfg::W_BYTES + 16 * o) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
@@ -257,63 +349,130 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 
     // The tensor memory is held before a dependent kernel may start: one that started
     // first and took it would wait for this one, which would wait for it.
-    FewItem item = {0, a.T, 0};
-    if (KIND != FEW_DOWN) {
+    if (Cfg::QUANT) {
         pdl_wait();
         pdl_launch_dependents();
     }
-    if (KIND == FEW_UP && blockIdx.y == 0)
+    // down, codes: the kernel before this one (up; the quantizer) waited for its own
+    // predecessor before it let this one start, so the ids and the weights are complete
+    // and only what that kernel writes has to be waited for
+    if (KIND == FEW_UP)
         for (int i = int(blockIdx.x) * Cfg::THREADS + tid; i < a.T * a.tiles_h;
              i += int(gridDim.x) * Cfg::THREADS)
             a.count[i] = 0;
-    // down: the ids (like the weights) were complete before the up kernel began, which
-    // waited for its predecessor before it let this one start
-    if (KIND != FEW_LINEAR) {
-        // its scratch is the first stage's weight tile, which the copies below overwrite
-        item = few_plan(plan, reinterpret_cast<int16_t *>(smem), a.ids, a.T, a.k, a.E,
-                        int(blockIdx.y));
-        fence_proxy_async_smem();
+    const int n_tiles = a.N / 128, tiles = n_tiles / RT;
+    int items = tiles;
+    if (Cfg::EXPERTS) {
+        for (int i = tid; i < a.T * a.k; i += Cfg::THREADS) {
+            const int v = a.ids[i];
+            const bool ok = v >= 0 && v < a.E;
+            id[i] = int16_t(ok ? v : -1);
+            if (ok)
+                atomicAdd(&count[v], 1);
+        }
+        __syncthreads();
+        if (warp == 4) {
+            const int n = few_units<NT>(count, a.E, units, lane);
+            if (lane == 0)
+                unit_count = n;
+        }
+        __syncthreads();
+        items *= unit_count;
+    }
+    // This CTA's items are first, first + step, ...; its part of their reduction is the
+    // blocks lo .. lo + nkb - 1.  Blocks are counted through all its items.
+    const int first = int(blockIdx.x) / split, step = int(gridDim.x) / split;
+    const int lo = a.KB * rank / split, nkb = a.KB * (rank + 1) / split - lo;
+    const int blocks = first < items ? ((items - 1 - first) / step + 1) * nkb : 0;
+    // A place in that walk: an item, and the block within its part.
+    struct Walk {
+        int item, i, tile;
+        FewUnit u;
+    };
+    const auto enter = [&](Walk &w, int item) {
+        w.item = item;
+        w.u = {0, 0, a.T};
+        w.tile = item;
+        if (Cfg::EXPERTS && item < items) {
+            const int unit = item / tiles;
+            w.u = FewUnit::of(units[unit]);
+            w.tile = item - unit * tiles;
+        }
+    };
+    const auto start = [&](int i) {
+        Walk w;
+        enter(w, first);
+        w.i = i;
+        return w;
+    };
+    const auto advance = [&](Walk &w, int by) {
+        w.i += by;
+        while (w.i >= nkb) {
+            w.i -= nkb;
+            enter(w, w.item + step);
+        }
+    };
+    // MMA columns in use: whole groups of 16
+    const auto columns = [](int rows) { return NT <= 16 ? 16 : (rows + 15) / 16 * 16; };
+    const auto load_weights = [&](const Walk &w, int s) {
+        const int row = w.u.expert * a.N + w.tile * 128;
+        uint8_t *dst = smem + s * Cfg::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[s], Cfg::W_BYTES + (Cfg::QUANT ? 0 : Cfg::X_BYTES));
+        tma_load_2d(dst, &tmW, &full[s], (lo + w.i) * 128, row);
+        if (KIND == FEW_UP)
+            tma_load_2d(dst + 128 * 128, &tmW, &full[s], (lo + w.i) * 128, row + a.N / 2);
+    };
+    // weights do not wait for the order of the rows, nor for the kernel before
+    const int early = min(STAGES, blocks);
+    if (warp == 4 && lane == 0) {
+        Walk w = start(0);
+        for (int n = 0; n < early; ++n, advance(w, 1))
+            load_weights(w, n);
+    }
+    if (Cfg::EXPERTS) {
+        if (warp == 0)
+            few_order(id, a.T * a.k, count, order, lane);
         __syncthreads();
     }
 
-    const int lo = a.KB * rank / split, hi = a.KB * (rank + 1) / split;
-    const int nkb = item.expert < 0 ? 0 : hi - lo;
-    const int n_tiles = a.N / 128;
-    const int wrow = item.expert * a.N + tile * 128;  // up: of the gate rows
-
     if (warp < 4) {
         // ------------------------------------------------------------- promotion
-        float acc[RT][NT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-                acc[r][c] = 0.0f;
-        if (nkb > 0) {
+        Walk at;
+        for (int n = 0, item = first; n < blocks; item += step) {
+            enter(at, item);
+            const FewUnit u = at.u;
+            const int tile = at.tile, cols = columns(u.rows);
+            float2 acc[RT][NT / 2];
             const float *sw[RT];
             float next[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                sw[r] = a.sw + (size_t(item.expert) * n_tiles + tile + r * (n_tiles / 2)) * a.KB + lo;
+#pragma unroll
+                for (int c = 0; c < NT / 2; ++c)
+                    acc[r][c] = make_float2(0.0f, 0.0f);
+                sw[r] = a.sw + (size_t(u.expert) * n_tiles + tile + r * tiles) * a.KB + lo;
                 next[r] = __ldg(sw[r]);
             }
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % STAGES, b = i % NBUF;
-                float cur[RT];
+            for (int i = 0; i < nkb; ++i, ++n) {
+                const int s = n % STAGES, b = n % NBUF;
+                float2 cur[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    cur[r] = next[r];
+                    cur[r] = make_float2(next[r], next[r]);
                     if (i + 1 < nkb)
                         next[r] = __ldg(sw[r] + i + 1);
                 }
-                // the stage's full barrier cannot run ahead: it waits for this warp below
+                // The stage's full barrier cannot run ahead: it waits for this warp below.
+                // After a wait that ran out the blocks are gone through without waiting, so
+                // that the warps meet at their barriers all the same.
                 const bool ok =
-                    mbar_wait_bounded(&full[s], uint32_t(i / STAGES) & 1u, abort_flag, &g_few_error,
+                    !*abort_flag &&
+                    mbar_wait_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
                                       FERR_PROMO, FEW_WAIT_NS) &&
-                    mbar_wait_bounded(&tfull[b], uint32_t(i / NBUF) & 1u, abort_flag, &g_few_error,
+                    mbar_wait_bounded(&tfull[b], uint32_t(n / NBUF) & 1u, abort_flag, &g_few_error,
                                       FERR_PROMO, FEW_WAIT_NS);
                 if (!__all_sync(0xffffffffu, ok))
-                    break;
+                    continue;
                 tc_fence_after();
                 const uint32_t taddr =
                     tmem_base + (uint32_t(warp * 32) << 16) + uint32_t(b * RT * NT);
@@ -321,82 +480,105 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 // 16 columns at a time: the sums already take RT x NT registers
 #pragma unroll
                 for (int c0 = 0; c0 < NT; c0 += 16) {
-                    uint32_t v[RT][16];
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        tmem_ld_32x32b_x16(taddr + uint32_t(r * NT + c0), v[r]);
-                    tmem_wait_ld();
-                    if (c0 + 16 == NT) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&tempty[b]);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const float4 x4 = xs4[(c0 + c) / 4];
-                        const float xc[4] = {x4.x, x4.y, x4.z, x4.w};
+                    if (c0 < cols) {
+                        uint32_t v[RT][16];
 #pragma unroll
                         for (int r = 0; r < RT; ++r)
+                            tmem_ld_32x32b_x16(taddr + uint32_t(r * NT + c0), v[r]);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                acc[r][c0 + c + q] = fmaf(__uint_as_float(v[r][c + q]),
-                                                          cur[r] * xc[q], acc[r][c0 + c + q]);
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 x4 = xs4[(c0 + c) / 4];
+                            const float2 xc[2] = {make_float2(x4.x, x4.y), make_float2(x4.z, x4.w)};
+#pragma unroll
+                            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    float2 &o = acc[r][(c0 + c) / 2 + q];
+                                    o = __ffma2_rn(make_float2(__uint_as_float(v[r][c + 2 * q]),
+                                                               __uint_as_float(v[r][c + 2 * q + 1])),
+                                                   __fmul2_rn(cur[r], xc[q]), o);
+                                }
+                        }
                     }
                 }
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    mbar_arrive(&tempty[b]);
                     mbar_arrive(&empty[s]);
+                }
             }
-            // Every product of this CTA is done (the last buffer was full), so no copy or
-            // MMA touches the stages any more: they take the sums, [RT][NT][128].
-            float *red = reinterpret_cast<float *>(smem);
+            if (split > 1) {
+                // The only item: every product of this CTA is done (the last buffer was
+                // full), so the stages are free to take its parts, [RT][NT][128].
+                float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-                    if (c < item.rows)
-                        red[(r * NT + c) * 128 + tid] = acc[r][c];
+                    for (int c = 0; c < NT; c += 2) {
+                        if (c < u.rows)
+                            part[(r * NT + c) * 128 + tid] = acc[r][c / 2].x;
+                        if (c + 1 < u.rows)
+                            part[(r * NT + c + 1) * 128 + tid] = acc[r][c / 2].y;
+                    }
+                continue;
+            }
+#pragma unroll
+            for (int c = 0; c < NT; c += 2) {
+                float2 v = acc[0][c / 2];
+                if (c < u.rows) {
+                    if (KIND == FEW_UP)
+                        v = make_float2(swiglu(v.x, acc[RT - 1][c / 2].x),
+                                        swiglu(v.y, acc[RT - 1][c / 2].y));
+                    red[c * 128 + tid] = v.x;
+                }
+                if (c + 1 < u.rows)
+                    red[(c + 1) * 128 + tid] = v.y;
+            }
+            promo_sync();
+            for (int r = warp; r < u.rows; r += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(red + r * 128 + 4 * lane);
+                if (KIND == FEW_UP)
+                    few_store_h(a, u.base + r, tile, lane, v);
+                else if (KIND == FEW_DOWN)
+                    few_combine(a, order[u.base + r], tile, lane, v);
+                else
+                    few_store(a, r, tile, lane, v);
+            }
+            promo_sync();  // the next item's sums may take their place
         }
     } else if (warp == 4) {
         // -------------------------------------------------------------- producer
-        if (lane == 0 && nkb > 0) {
-            const int bytes = Cfg::W_BYTES + (KIND == FEW_DOWN ? Cfg::X_BYTES : 0);
-            int ahead = 0;  // down: stages whose weights were asked for before the wait
-            if (KIND == FEW_DOWN) {
-                ahead = min(STAGES, nkb);
-                for (int i = 0; i < ahead; ++i) {
-                    mbar_arrive_expect_tx(&full[i], bytes);
-                    tma_load_2d(smem + i * Cfg::STAGE_BYTES, &tmW, &full[i], (lo + i) * 128, wrow);
-                }
+        if (lane == 0 && blocks > 0) {
+            if (!Cfg::QUANT) {
                 pdl_wait();
                 pdl_launch_dependents();
             }
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % STAGES;
-                uint8_t *sw = smem + s * Cfg::STAGE_BYTES;
-                if (i >= ahead) {
-                    if (!mbar_wait_bounded(&empty[s], (uint32_t(i / STAGES) & 1u) ^ 1u, abort_flag,
+            Walk w = start(0);
+            for (int n = 0; n < blocks; ++n, advance(w, 1)) {
+                const int s = n % STAGES;
+                if (n >= early) {
+                    if (!mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
                                            &g_few_error, FERR_PRODUCER, FEW_WAIT_NS))
                         break;
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    tma_load_2d(sw, &tmW, &full[s], (lo + i) * 128, wrow);
-                    if (KIND == FEW_UP)
-                        tma_load_2d(sw + 128 * 128, &tmW, &full[s], (lo + i) * 128, wrow + a.N / 2);
+                    load_weights(w, s);
                 }
-                if (KIND == FEW_DOWN)
-                    tma_load_2d(sw + Cfg::W_BYTES, &tmH, &full[s], (lo + i) * 128, item.base);
+                if (!Cfg::QUANT)
+                    tma_load_2d(smem + s * Cfg::STAGE_BYTES + Cfg::W_BYTES, &tmH, &full[s],
+                                (lo + w.i) * 128, w.u.base);
             }
         }
     } else if (warp == 5) {
         // ------------------------------------------------------------------- MMA
         if (lane == 0) {
-            constexpr uint32_t idesc = make_idesc_e4m3(128, NT, 0);
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % STAGES, b = i % NBUF;
-                if (!mbar_spin_bounded(&full[s], uint32_t(i / STAGES) & 1u, abort_flag, &g_few_error,
+            Walk w = start(0);
+            for (int n = 0; n < blocks; ++n, advance(w, 1)) {
+                const int s = n % STAGES, b = n % NBUF;
+                const uint32_t idesc = make_idesc_e4m3(128, columns(w.u.rows), 0);
+                if (!mbar_spin_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
                                        FERR_MMA_FULL, FEW_WAIT_NS) ||
-                    !mbar_spin_bounded(&tempty[b], (uint32_t(i / NBUF) & 1u) ^ 1u, abort_flag,
+                    !mbar_spin_bounded(&tempty[b], (uint32_t(n / NBUF) & 1u) ^ 1u, abort_flag,
                                        &g_few_error, FERR_MMA_TEMPTY, FEW_WAIT_NS))
                     break;
                 tc_fence_after();
@@ -410,54 +592,54 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                                       make_smem_desc_sw128(w_addr + r * 128 * 128 + k * 32, 16, 1024),
                                       make_smem_desc_sw128(x_addr + k * 32, 16, 1024), idesc,
                                       k > 0 ? 1u : 0u);
-                mma_commit(&empty[s]);
                 mma_commit(&tfull[b]);
             }
         }
-    } else if (KIND != FEW_DOWN) {
+    } else if (Cfg::QUANT) {
         // -------------------------------------------- quantize the tokens' groups
-        // Half-warp w takes rows w, w + 8, ...; lane `sub` of it 8 neighbouring values.
-        const int sub = lane & 15, first = (warp - 6) * 2;
-        const int row0 = first + (lane >> 4);
-        constexpr int ROWS = NT / 8;
-        const uint4 *x4 = reinterpret_cast<const uint4 *>(a.x);
-        int src[ROWS];  // in pieces of 8 values; -1: no row
-        uint4 v[ROWS];
+        // One block per warp in turn; four row pairs at a time, the next four's values under
+        // way meanwhile.
+        constexpr int P = 4;
+        const uint4 *x4 = reinterpret_cast<const uint4 *>(a.x) + lo * 16 + (lane & 15);
+        const auto fetch = [&](const Walk &w, int r0, uint4 (&v)[P]) {
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-            const int r = row0 + 8 * q;
-            const int t = KIND == FEW_LINEAR ? r : (r < item.rows ? int(plan.row_token[r]) : 0);
-            src[q] = r < item.rows ? t * (a.K / 8) + lo * 16 + sub : -1;
-            v[q] = nkb > 0 && src[q] >= 0 ? __ldg(x4 + src[q]) : make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < P; ++q) {
+                const int r = r0 + 2 * q + (lane >> 4);
+                v[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (w.item < items && r < w.u.rows) {
+                    const int t = KIND == FEW_UP ? int(order[w.u.base + r]) / a.k : r;
+                    v[q] = __ldg(x4 + (t * (a.K / 8) + w.i * 16));
+                }
+            }
+        };
+        uint4 v[P], ahead[P];
+        Walk w = {}, next;
+        if (blocks > 0) {
+            w = start(0);
+            advance(w, warp - 6);
+            fetch(w, 0, v);
         }
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % STAGES;
-            const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(i / STAGES) & 1u) ^ 1u, abort_flag,
+        for (int n = warp - 6; n < blocks; n += Cfg::ACT_WARPS, w = next) {
+            const int s = n % STAGES, rows = w.u.rows;
+            next = w;
+            advance(next, Cfg::ACT_WARPS);
+            const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
                                               &g_few_error, FERR_ACT, FEW_WAIT_NS);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             uint8_t *sx = smem + s * Cfg::STAGE_BYTES + Cfg::W_BYTES;
-#pragma unroll
-            for (int q = 0; q < ROWS; ++q) {
-                if (first + 8 * q >= item.rows)  // neither half-warp has a row
-                    break;
-                const int r = row0 + 8 * q;
-                const uint4 w = v[q];
-                if (src[q] >= 0 && i + 1 < nkb)  // the next block's values are under way meanwhile
-                    v[q] = __ldg(x4 + src[q] + (i + 1) * 16);
-                uint32_t m2 = __vmaxu2(absmax2(w.x, w.y), absmax2(w.z, w.w));
-#pragma unroll
-                for (int o = 8; o >= 1; o >>= 1)
-                    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-                const float amax = halves_max_to_float(m2);
-                const float sc = scale_of_amax(amax);
-                if (r < item.rows) {
-                    const uint2 codes = amax != 0.0f ? quant8(w, GroupDiv(sc)) : make_uint2(0u, 0u);
-                    *reinterpret_cast<uint2 *>(sx + r * 128 + (((sub >> 1) ^ (r & 7)) << 4) +
-                                               (sub & 1) * 8) = codes;
-                    if (sub == 0)
-                        xs[s * NT + r] = sc;
+            for (int r0 = 0; r0 < rows; r0 += 2 * P) {
+                const bool more = r0 + 2 * P < rows;
+                fetch(more ? w : next, more ? r0 + 2 * P : 0, ahead);
+                if (r0 + 2 < rows) {
+                    few_quant<P>(v, r0, rows, lane, sx, xs + s * NT);
+                } else {
+                    const uint4 one[1] = {v[0]};
+                    few_quant<1>(one, r0, rows, lane, sx, xs + s * NT);
                 }
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+                    v[q] = ahead[q];
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -465,22 +647,25 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 mbar_arrive(&full[s]);
         }
     } else {
-        // ------------------------------------------------------- scales of h (down)
+        // --------------------------------------------------- scales of the codes
         pdl_wait();
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % STAGES;
-            const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(i / STAGES) & 1u) ^ 1u, abort_flag,
+        Walk w = {};
+        if (blocks > 0)
+            w = start(0);
+        for (int n = 0; n < blocks; ++n, advance(w, 1)) {
+            const int s = n % STAGES;
+            const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
                                               &g_few_error, FERR_ACT, FEW_WAIT_NS);
             if (!__all_sync(0xffffffffu, ok))
                 break;
-            for (int r = lane; r < item.rows; r += 32)
-                xs[s * NT + r] = a.hs[size_t(lo + i) * (a.T * a.k) + item.base + r];
+            for (int r = lane; r < w.u.rows; r += 32)
+                xs[s * NT + r] = a.sx[size_t(lo + w.i) * a.sx_rows + w.u.base + r];
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&full[s]);
         }
     }
-    if (KIND == FEW_DOWN)
+    if (!Cfg::QUANT)
         pdl_wait();
     tc_fence_before();
     __syncthreads();
@@ -490,117 +675,78 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         while (global_timer_ns() - t0 < FEW_DRAIN_NS) {
         }
     }
-    if (split > 1)
-        cluster_sync();
-
-    // ------------------------------------------------- join the parts, finish the rows
-    // One warp per row; lane l has columns 4 l .. 4 l + 3 of the tile.
-    const uint32_t red0 = smem_u32(smem);
-    for (int r = rank + split * warp; r < item.rows && item.expert >= 0; r += split * WARPS) {
-        float4 sum[RT];
-#pragma unroll
-        for (int q = 0; q < RT; ++q) {
-            sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const uint32_t at = red0 + uint32_t(((q * NT + r) * 128 + 4 * lane) * 4);
-            for (int p = 0; p < split; ++p) {
-                const float4 v = ld_cluster_v4(mapa_shared(at, uint32_t(p)));
-                sum[q].x += v.x;
-                sum[q].y += v.y;
-                sum[q].z += v.z;
-                sum[q].w += v.w;
-            }
-        }
-        if (KIND == FEW_LINEAR) {
-            *reinterpret_cast<uint2 *>(a.y + size_t(r) * a.N + tile * 128 + 4 * lane) = bf16x4(sum[0]);
-        } else if (KIND == FEW_UP) {
-            const float g[4] = {sum[0].x, sum[0].y, sum[0].z, sum[0].w};
-            const float u[4] = {sum[RT - 1].x, sum[RT - 1].y, sum[RT - 1].z, sum[RT - 1].w};
-            float h[4], amax = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                h[q] = g[q] / (1.0f + expf(-g[q])) * u[q];
-                amax = fmaxf(amax, fabsf(h[q]));
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // h is kept in FP32 up to its one rounding onto E4M3
-            const float sc = __fdiv_rn(amax, 448.0f);
-            uint32_t codes = 0u;
-            if (sc != 0.0f)
-                codes = cvt_e4m3x2(__fdiv_rn(h[0], sc), __fdiv_rn(h[1], sc)) |
-                        (cvt_e4m3x2(__fdiv_rn(h[2], sc), __fdiv_rn(h[3], sc)) << 16);
-            const size_t row = size_t(item.base + r);
-            *reinterpret_cast<uint32_t *>(a.hq + row * (a.N / 2) + tile * 128 + 4 * lane) = codes;
-            if (lane == 0)
-                a.hs[size_t(tile) * (a.T * a.k) + row] = sc;
-        } else {
-            // The pair's product goes to memory; the warp that brings a token's last one
-            // adds them all, in the order of the choices.
-            const int t = plan.row_token[r];
-            const size_t col = size_t(tile) * 128 + 4 * lane;
-            *reinterpret_cast<float4 *>(a.part + size_t(plan.row_pair[r]) * a.N + col) = sum[0];
-            float w;
-            const int id = few_choice(a, t, lane, w);
-            const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
-            __threadfence();
-            __syncwarp();
-            int done = 0;
-            if (lane == 0)
-                done = atomicAdd(&a.count[t * n_tiles + tile], 1) + 1;
-            done = __shfl_sync(0xffffffffu, done, 0);
-            if (done == __popc(live)) {
-                __threadfence();
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int j = 0; j < a.k; ++j) {
-                    if (!((live >> j) & 1u))
-                        continue;
-                    const float wj = __shfl_sync(0xffffffffu, w, j);
-                    const float4 v = __ldcg(
-                        reinterpret_cast<const float4 *>(a.part + size_t(t * a.k + j) * a.N + col));
-                    y.x = fmaf(wj, v.x, y.x);
-                    y.y = fmaf(wj, v.y, y.y);
-                    y.z = fmaf(wj, v.z, y.z);
-                    y.w = fmaf(wj, v.w, y.w);
-                }
-                *reinterpret_cast<uint2 *>(a.y + size_t(t) * a.N + col) = bf16x4(y);
-            }
-        }
-    }
-    if (KIND == FEW_DOWN && blockIdx.y == 0 && rank == 0) {
-        // tokens that chose no expert
-        for (int t = warp; t < a.T; t += WARPS) {
-            float w;
-            if (!__any_sync(0xffffffffu, few_choice(a, t, lane, w) >= 0))
-                *reinterpret_cast<uint2 *>(a.y + size_t(t) * a.N + tile * 128 + 4 * lane) =
-                    make_uint2(0u, 0u);
-        }
-    }
-    if (split > 1)
-        cluster_sync();  // no peer reads this CTA's sums any more
-    else
-        __syncthreads();
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc<1>(tmem_base, Cfg::TMEM_COLS);
     }
+    if (split > 1) {
+        // ---------------------------------------------------- join the cluster's parts
+        cluster_sync();
+        if (first < items) {
+            Walk w;
+            enter(w, first);
+            const FewUnit u = w.u;
+            const int tile = w.tile;
+            const uint32_t part0 = smem_u32(smem);
+            for (int r = rank + split * warp; r < u.rows; r += split * WARPS) {
+                float4 sum[RT];
+#pragma unroll
+                for (int q = 0; q < RT; ++q) {
+                    const uint32_t at = part0 + uint32_t(((q * NT + r) * 128 + 4 * lane) * 4);
+                    float4 v[FEW_MAX_SPLIT];
+#pragma unroll
+                    for (int p = 0; p < FEW_MAX_SPLIT; ++p)
+                        v[p] = p < split ? ld_cluster_v4(mapa_shared(at, uint32_t(p)))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                    sum[q] = v[0];
+#pragma unroll
+                    for (int p = 1; p < FEW_MAX_SPLIT; ++p) {
+                        sum[q].x += v[p].x;
+                        sum[q].y += v[p].y;
+                        sum[q].z += v[p].z;
+                        sum[q].w += v[p].w;
+                    }
+                }
+                const float4 g = sum[0], up = sum[RT - 1];
+                if (KIND == FEW_UP)
+                    few_store_h(a, u.base + r, tile, lane,
+                                make_float4(swiglu(g.x, up.x), swiglu(g.y, up.y), swiglu(g.z, up.z),
+                                            swiglu(g.w, up.w)));
+                else if (KIND == FEW_DOWN)
+                    few_combine(a, order[u.base + r], tile, lane, g);
+                else
+                    few_store(a, r, tile, lane, g);
+            }
+        }
+        cluster_sync();  // no peer reads this CTA's parts any more
+    }
+    if (KIND == FEW_DOWN)
+        // tokens that chose no expert: one warp for each of their tiles
+        for (int i = int(blockIdx.x) * WARPS + warp; i < a.T * tiles; i += int(gridDim.x) * WARPS)
+            if (!__any_sync(0xffffffffu, few_choice(a, i / tiles, lane) >= 0))
+                few_store(a, i / tiles, i % tiles, lane, make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
 // ------------------------------------------------------------------- host side
 
-// CTAs per tile: the reduction is split until the tiles fill the GPU, with two blocks
+// The linear quantizes its tokens itself up to this many.  Beyond, every tile's CTAs
+// would quantize them anew for longer than their weights take to arrive, and the codes
+// come from the quantizer's kernel, whose time the next one's start hides.
+constexpr int FEW_QUANT_TOKENS = 16;
+
+// CTAs per item: the reduction is split until the items fill the GPU, with two blocks
 // of 128 left for each CTA at least.
-static int few_split(int64_t items, int64_t KB, int num_sms)
+static int few_split(int64_t items, int64_t KB, int64_t slots)
 {
     int s = 1;
-    while (s < 8 && items * s * 2 <= 2 * num_sms && KB >= 4 * s)
+    while (s < FEW_MAX_SPLIT && items * s * 2 <= slots && KB >= 4 * s)
         s *= 2;
     return s;
 }
 
 template <class Cfg>
-static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *hq, const FewArgs &a,
-                           int64_t tiles, int64_t slots, cudaStream_t stream, int num_sms)
+static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *codes, const FewArgs &a,
+                           cudaStream_t stream, int num_sms)
 {
     auto kern = few_kernel<Cfg>;
     static LaunchCache cache;
@@ -617,10 +763,15 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *hq, 
     CUtensorMap tw, th;
     if (!codes_map(&tw, w, uint64_t(w_rows), uint64_t(a.K), 128))
         return cudaErrorInvalidValue;
-    th = tw;  // not used but by down
-    if (Cfg::KIND == FEW_DOWN && !codes_map(&th, hq, uint64_t(a.T) * a.k, uint64_t(a.K), Cfg::NT))
+    th = tw;  // only used where the tokens' codes are in memory
+    if (!Cfg::QUANT && !codes_map(&th, codes, uint64_t(a.sx_rows), uint64_t(a.K), Cfg::NT))
         return cudaErrorInvalidValue;
-    const int split = few_split(tiles * slots, a.KB, num_sms);
+    // The most items there may be: an expert's rows make whole units but for one.  A
+    // cluster takes one item at most, so those that split theirs have to cover them all.
+    const int64_t pairs = int64_t(a.T) * a.k;
+    const int64_t units = Cfg::EXPERTS ? (pairs < a.E ? pairs : a.E) + pairs / Cfg::NT : 1;
+    const int64_t items = units * (a.N / 128 / Cfg::RT), slots = int64_t(num_sms) * Cfg::BLOCKS;
+    const int split = few_split(items, a.KB, slots);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     set_pdl(at[0]);
@@ -628,7 +779,7 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *hq, 
     at[1].val.clusterDim.x = unsigned(split);
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(tiles * split), unsigned(slots));
+    cfg.gridDim = dim3(unsigned(split > 1 || items < slots ? items * split : slots));
     cfg.blockDim = dim3(Cfg::THREADS);
     cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = stream;
@@ -638,20 +789,14 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *hq, 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int KIND>
-static cudaError_t run_few_kind(const uint8_t *w, int64_t w_rows, const uint8_t *hq,
-                                const FewArgs &a, int64_t tiles, int64_t slots, cudaStream_t stream,
-                                int num_sms)
+size_t linear_few_workspace(int T, int64_t K)
 {
-    if (a.T <= 16)
-        return run_few<FewCfg<KIND, 16>>(w, w_rows, hq, a, tiles, slots, stream, num_sms);
-    if (a.T <= 32)
-        return run_few<FewCfg<KIND, 32>>(w, w_rows, hq, a, tiles, slots, stream, num_sms);
-    return run_few<FewCfg<KIND, 64>>(w, w_rows, hq, a, tiles, slots, stream, num_sms);
+    // codes, then scales
+    return T <= FEW_QUANT_TOKENS ? 0 : size_t(T) * K + size_t(T) * (K / 128) * 4;
 }
 
 cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const float *sw, void *y,
-                              int64_t N, int64_t K, cudaStream_t stream, int num_sms)
+                              int64_t N, int64_t K, void *workspace, cudaStream_t stream, int num_sms)
 {
     FewArgs a = {};
     a.x = static_cast<const __nv_bfloat16 *>(x);
@@ -663,7 +808,17 @@ cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const flo
     a.N = int(N);
     a.K = int(K);
     a.KB = int(K / 128);
-    return run_few_kind<FEW_LINEAR>(qw, N, nullptr, a, N / 128, 1, stream, num_sms);
+    if (T <= FEW_QUANT_TOKENS)
+        return run_few<FewCfg<FEW_LINEAR, 16>>(qw, N, nullptr, a, stream, num_sms);
+    uint8_t *q = static_cast<uint8_t *>(workspace);
+    float *s = reinterpret_cast<float *>(q + size_t(T) * K);
+    a.sx = s;
+    a.sx_rows = T;
+    const cudaError_t e = launch_quant_act(x, T, K, q, s, stream, num_sms);
+    if (e != cudaSuccess)
+        return e;
+    return T <= 32 ? run_few<FewCfg<FEW_CODES, 32>>(qw, N, q, a, stream, num_sms)
+                   : run_few<FewCfg<FEW_CODES, 64>>(qw, N, q, a, stream, num_sms);
 }
 
 // The workspace of the layer: codes and scales of h, each pair's product, counters.
@@ -692,7 +847,6 @@ cudaError_t launch_moe_few(const void *x, int T, const uint8_t *w1, const float 
 {
     const FewSpace space(T, k, H, I);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int64_t slots = int64_t(T) * k < E ? int64_t(T) * k : E;  // experts that can be hit
     FewArgs a = {};
     a.x = static_cast<const __nv_bfloat16 *>(x);
     a.sw = s1;
@@ -710,14 +864,19 @@ cudaError_t launch_moe_few(const void *x, int T, const uint8_t *w1, const float 
     a.K = int(H);
     a.KB = int(H / 128);
     a.tiles_h = int(H / 128);
-    cudaError_t e = run_few_kind<FEW_UP>(w1, E * 2 * I, ws, a, I / 128, slots, stream, num_sms);
+    cudaError_t e = T <= 16
+        ? run_few<FewCfg<FEW_UP, 16>>(w1, E * 2 * I, nullptr, a, stream, num_sms)
+        : run_few<FewCfg<FEW_UP, 32>>(w1, E * 2 * I, nullptr, a, stream, num_sms);
     if (e != cudaSuccess)
         return e;
     a.sw = s2;
     a.N = int(H);
     a.K = int(I);
     a.KB = int(I / 128);
-    return run_few_kind<FEW_DOWN>(w2, E * H, ws, a, H / 128, slots, stream, num_sms);
+    a.sx = a.hs;
+    a.sx_rows = T * k;
+    return T <= 16 ? run_few<FewCfg<FEW_DOWN, 16>>(w2, E * H, ws, a, stream, num_sms)
+                   : run_few<FewCfg<FEW_DOWN, 32>>(w2, E * H, ws, a, stream, num_sms);
 }
 
 cudaError_t read_and_clear_few_error(int *value)

@@ -24,7 +24,9 @@ cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t
 // Few-token linear and the two kernels of the few-token expert layer.
 constexpr int kFewMaxTokens = 64;
 cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const float *sw, void *y,
-                              int64_t N, int64_t K, cudaStream_t stream, int num_sms);
+                              int64_t N, int64_t K, void *workspace, cudaStream_t stream,
+                              int num_sms);
+size_t linear_few_workspace(int T, int64_t K);
 size_t moe_few_workspace(int T, int k, int64_t H, int64_t I);
 cudaError_t launch_moe_few(const void *x, int T, const uint8_t *w1, const float *s1,
                            const uint8_t *w2, const float *s2, const int32_t *ids,

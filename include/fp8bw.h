@@ -221,14 +221,17 @@ int fp8_gemm_blockwise_e8m0(int mode, const uint8_t *a, const uint8_t *sa_e8m0,
  * ---- Few tokens: the linear of a decode step ----
  *
  * fp8_linear_few -- Y[M][N] = X . W^T for M = 1 .. FP8BW_FEW_TOKENS tokens (any such
- * number), in one launch: X is quantized inside the kernel exactly as fp8_quant_act
- * would (the same codes and scales), then multiplied as by fp8_gemm_blockwise(FPROP).
+ * number): X is quantized within the call exactly as fp8_quant_act would (the same
+ * codes and scales), then multiplied as by fp8_gemm_blockwise(FPROP).
  *   x [M][K] BF16     qw [N][K], sw [N/128][K/128] from fp8_quant_weight
  *   y [M][N] BF16, written, never read
- * M out of range returns FP8BW_ESHAPE.
+ *   workspace: fp8_linear_few_workspace(M, K) bytes (may be NULL if that is 0), not
+ *     shared with a call, or a captured graph, that may run at the same time
+ * M out of range returns FP8BW_ESHAPE; the size function then returns 0.
  */
+int64_t fp8_linear_few_workspace(int64_t M, int64_t K);
 int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void *y_bf16,
-                   int64_t M, int64_t N, int64_t K, void *stream);
+                   int64_t M, int64_t N, int64_t K, void *workspace, void *stream);
 
 /*
  * ---- Mixture of experts ----

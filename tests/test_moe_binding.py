@@ -26,12 +26,17 @@ P, ODD, NUL, S = C.c_void_p(0x10000), C.c_void_p(0x10008), C.c_void_p(0), C.c_vo
 
 def test_linear_few_arguments(L):
     f = L.fp8_linear_few
-    assert f(NUL, P, P, P, 1, 128, 128, S) == 1
-    assert f(P, P, P, NUL, 1, 128, 128, S) == 1
+    assert f(NUL, P, P, P, 1, 128, 128, P, S) == 1
+    assert f(P, P, P, NUL, 1, 128, 128, P, S) == 1
+    assert f(P, P, P, P, 64, 128, 128, NUL, S) == 1   # 64 tokens need a workspace
     for m, n, k in ((0, 128, 128), (65, 128, 128), (-1, 128, 128), (1, 100, 128), (1, 128, 0),
                     (1, (1 << 20) + 128, 128)):
-        assert f(P, P, P, P, m, n, k, S) == 3
-    assert f(ODD, P, P, P, 1, 128, 128, S) == 2
+        assert f(P, P, P, P, m, n, k, P, S) == 3
+    assert f(ODD, P, P, P, 1, 128, 128, P, S) == 2
+    assert f(P, P, P, P, 64, 128, 128, ODD, S) == 2
+    w = L.fp8_linear_few_workspace
+    assert w(0, 128) == 0 and w(65, 128) == 0 and w(64, 100) == 0
+    assert w(1, 128) == 0 and w(64, 256) >= 64 * 256 + 2 * 64 * 4
 
 
 def test_route_arguments(L):
@@ -160,6 +165,7 @@ def layer(**kw):
     lambda: layer(ids=z(4, 2, dtype=i32)),
     lambda: layer(weights=z(5, 3, dtype=f32)),
     lambda: fb.fp8_moe_few_workspace(65, 2, 128, 128),
+    lambda: fb.fp8_linear_few_workspace(65, 128),
 ], ids=lambda c: "")
 def test_sizes_are_refused(call):
     with pytest.raises(ValueError):

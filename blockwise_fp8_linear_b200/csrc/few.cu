@@ -12,24 +12,26 @@
 // tcgen05.mma takes a whole 128 x 32 weight tile and TMA streams weights straight into
 // shared memory without passing through registers.  An item of work is a tile of 128
 // weight rows (up: 128 gate rows and the 128 up rows beside them) for the tokens of one
-// expert.  CTAs, two to an SM, walk the items; the loads run ahead into the next item
-// while one is finished.  Where the items are fewer than the SMs can take, the CTAs of a
-// cluster split the reduction of one item between them and join their FP32 sums through
+// expert.  The experts' CTAs, one to an SM, walk the items; loads and products of the next item run
+// while one is finished.  Where the items are fewer than the SMs, the CTAs of a cluster
+// split the reduction of one item between them and join their FP32 sums through
 // distributed shared memory in a fixed order.
 //
 //   warps 0..3  promotion: partial sums of a 128-block from TMEM (thread = weight row),
 //               times weight scale x token scale, into FP32 sums in registers
 //   warp 4      TMA producer: weight tiles, and the tokens' codes where memory has them
-//   warp 5      MMA issuer
-//   warps 6..   linear, up: quantize the tokens' 1x128 groups into shared memory (the
+//   warps 5, 6  MMA issuers, each for one of the two TMEM buffers (one alone spends as
+//               long on a block's barriers as on its products and falls behind HBM)
+//   warps 7..   linear, up: quantize the tokens' 1x128 groups into shared memory (the
 //               arithmetic of fp8_quant_act), one block per warp in turn; otherwise one warp
 //               that loads the scales of the codes
+//   the rest    experts: finish the rows of an item
 //
-// The rows of the experts are the (token, choice) pairs sorted by expert, in pair order;
-// an item takes up to 32 of one expert's.  Every CTA sorts the ids for itself (they are
-// at most 2048) before its first item.  Columns of the MMA without a token hold whatever
-// the stage held before: columns do not mix, and theirs are not stored.  Every wait is
-// bounded.
+// An expert's rows are the tokens that chose it, in their order; an item takes up to 32
+// of them.  Every CTA works them out from the ids (at most 2048) before its first item:
+// a 64-bit mask of tokens per expert gives each token's row by counting bits.  Columns of
+// the MMA without a token hold whatever the stage held before: columns do not mix, and
+// theirs are not stored.  Every wait is bounded.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -47,7 +49,7 @@ namespace fp8bw {
 __device__ int g_few_error;  // first error code of a bounded wait in these kernels
 constexpr uint64_t FEW_WAIT_NS = 1000000000ull;
 constexpr uint64_t FEW_DRAIN_NS = 20000000ull;
-enum : int { FERR_PRODUCER = 31, FERR_MMA_FULL = 32, FERR_MMA_TEMPTY = 33, FERR_PROMO = 34, FERR_ACT = 35 };
+enum : int { FERR_PRODUCER = 31, FERR_MMA_FULL = 32, FERR_MMA_TEMPTY = 33, FERR_PROMO = 34, FERR_ACT = 35, FERR_FINISH = 36 };
 
 // FEW_CODES: the linear on codes that fp8_quant_act's kernel has made.
 enum : int { FEW_LINEAR = 0, FEW_UP = 1, FEW_DOWN = 2, FEW_CODES = 3 };
@@ -64,7 +66,7 @@ struct FewArgs {
     float *hs;               // [I/128][T*k] their scales (up writes)
     const float *sx;         // [K/128][sx_rows] scales of the codes (down, codes)
     int sx_rows;
-    float *part;             // [T*k][H] products of each pair (down)
+    float *part;             // [T*k][H] products of each row (down)
     int *count;              // [T][H/128] experts of the token that are done (down)
     int T, k, E;
     int N, K, KB;            // rows and columns of one expert's weight, K / 128
@@ -81,27 +83,33 @@ struct FewCfg {
     static constexpr int W_BYTES = RT * 128 * 128;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int BLOCKS = 2;                    // CTAs per SM
-    // (up has two, which leaves its promotion warps the registers for their sums)
+    // The linear's CTAs have one item each and share an SM with the next kernel's.
+    static constexpr int BLOCKS = EXPERTS ? 1 : 2;
+    static constexpr int ACT_WARP0 = 7;
     static constexpr int ACT_WARPS = KIND == FEW_LINEAR ? 4 : KIND == FEW_UP ? 2 : 1;
-    static constexpr int THREADS = (6 + ACT_WARPS) * 32;
+    static constexpr int FIN_WARP0 = ACT_WARP0 + ACT_WARPS;
+    // (up has three: 12 warps leave its promotion warps the registers for their sums)
+    static constexpr int FIN_WARPS = KIND == FEW_UP ? 3 : KIND == FEW_DOWN ? 4 : 0;
+    static constexpr int THREADS = (FIN_WARP0 + FIN_WARPS) * 32;
     static constexpr int NBUF = 2;
     static constexpr int TMEM_COLS = NBUF * RT * NT;    // 32 .. 128, a power of two
     // finished sums of one item, [NT][128]; before the first item, scratch of the plan
-    static constexpr int RED_BYTES = NT * 128 * 4;
+    static constexpr int RED_BYTES = EXPERTS ? NT * 128 * 4 : 0;
     static constexpr int MAX_PAIRS = !EXPERTS ? 0 : NT == 16 ? 16 * 32 : 64 * 32;
     static constexpr int MAX_UNITS = !EXPERTS ? 0 : (NT == 16 ? MAX_PAIRS : 1024) + MAX_PAIRS / NT;
-    static constexpr int FIXED = RED_BYTES + MAX_UNITS * 4 + MAX_PAIRS * 2 + 1024 + 512;
-    static constexpr int STAGES = (112 * 1024 - FIXED) / (STAGE_BYTES + NT * 4);
+    static constexpr int FIXED = RED_BYTES + (EXPERTS ? 1024 * 10 : 0) + MAX_UNITS * 4 + MAX_PAIRS + 1536;
+    static constexpr int STAGES = (226 / BLOCKS * 1024 - FIXED) / (STAGE_BYTES + NT * 4);
     static constexpr int RED_OFF = STAGES * STAGE_BYTES;
     static constexpr int XS_OFF = RED_OFF + RED_BYTES;          // [STAGES][NT] token scales
-    static constexpr int UNIT_OFF = XS_OFF + STAGES * NT * 4;   // [MAX_UNITS] unsigned
-    static constexpr int ORDER_OFF = UNIT_OFF + MAX_UNITS * 4;  // [MAX_PAIRS] 16-bit
-    static constexpr int BAR_OFF = ORDER_OFF + MAX_PAIRS * 2;
-    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 2 * NBUF) * 8 + 16;
-    static_assert(RT * RED_BYTES <= STAGES * STAGE_BYTES, "a cluster's parts take the stages");
-    static_assert(!EXPERTS || MAX_PAIRS * 2 + 1024 * 4 <= RED_BYTES, "the plan's scratch");
-    static_assert(TMEM_COLS >= 32 && TMEM_COLS * BLOCKS <= 512, "tensor memory of an SM");
+    static constexpr int MASK_OFF = XS_OFF + STAGES * NT * 4;   // [1024][2] unsigned
+    static constexpr int BASE_OFF = MASK_OFF + (EXPERTS ? 1024 * 8 : 0);  // [1024] 16-bit
+    static constexpr int UNIT_OFF = BASE_OFF + (EXPERTS ? 1024 * 2 : 0);  // [MAX_UNITS] unsigned
+    static constexpr int TOKEN_OFF = UNIT_OFF + MAX_UNITS * 4;  // [MAX_PAIRS] 8-bit
+    static constexpr int BAR_OFF = TOKEN_OFF + MAX_PAIRS;
+    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 2 * NBUF + 2) * 8 + 16;
+    static_assert(BAR_OFF % 8 == 0, "barriers are 8-byte words");
+    static_assert(RT * NT * 128 * 4 <= STAGES * STAGE_BYTES, "a cluster's parts take the stages");
+    static_assert(MAX_PAIRS * 2 <= RED_BYTES, "the plan's scratch");
     // 228 KB per SM, 1 KB of it reserved per CTA
     static_assert((SMEM + 1024 + 64) * BLOCKS <= 228 * 1024, "shared memory of an SM");
 };
@@ -120,52 +128,47 @@ struct FewUnit {
     }
 };
 
-// Counts per expert (n[E], shared) -> where each expert's rows start (in its place) and
-// the units of at most NT rows.  One warp; returns how many units there are.
-template <int NT>
-__device__ __forceinline__ int few_units(int *n, int E, uint32_t *units, int lane)
-{
-    int row0 = 0, unit0 = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
-        const int c = e < E ? n[e] : 0, u = (c + NT - 1) / NT;
-        int sum = u << 16 | c;  // both sums at once: at most 2048 rows and 1088 units
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, o);
-            sum += lane >= o ? up : 0;
-        }
-        const int row = row0 + (sum & 0xFFFF) - c, unit = unit0 + (sum >> 16) - u;
-        if (e < E)
-            n[e] = row;
-        for (int i = 0; i < u; ++i)
-            units[unit + i] = FewUnit::pack(e, row + i * NT, min(NT, c - i * NT));
-        const int all = __shfl_sync(0xffffffffu, sum, 31);
-        row0 += all & 0xFFFF;
-        unit0 += all >> 16;
-    }
-    return unit0;
-}
+// The experts' rows, in shared memory.
+struct FewPlan {
+    uint32_t *mask;   // [E][2] the tokens that chose each expert
+    uint16_t *base;   // [E] its first row
+    uint32_t *units;  // the units of all experts, in expert order
+    uint8_t *token;   // of each row
 
-// Places the pairs: order[row] = pair, in pair order within an expert.  One warp; at[e]
-// is the expert's next row.
-__device__ __forceinline__ void few_order(const int16_t *id, int pairs, int *at, int16_t *order,
-                                          int lane)
-{
-    for (int p0 = 0; p0 < pairs; p0 += 32) {
-        const int e = p0 + lane < pairs ? int(id[p0 + lane]) : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        int row = 0;
-        if (e >= 0) {
-            row = at[e] + __popc(same & ((1u << lane) - 1u));
-            order[row] = int16_t(p0 + lane);
-        }
-        __syncwarp();
-        if (e >= 0 && lane == 31 - __clz(same))
-            at[e] = row + 1;
-        __syncwarp();
+    // How many of expert e's tokens come before t.
+    __device__ __forceinline__ int before(int e, int t) const
+    {
+        const uint32_t low = (1u << (t & 31)) - 1u;
+        return t < 32 ? __popc(mask[2 * e] & low) : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & low);
     }
-}
+    __device__ __forceinline__ int row(int e, int t) const { return base[e] + before(e, t); }
+
+    // Masks -> first rows and units of at most NT rows.  One warp; returns how many units.
+    template <int NT> __device__ __forceinline__ int make_units(int E, int lane) const
+    {
+        int row0 = 0, unit0 = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = e < E ? __popc(mask[2 * e]) + __popc(mask[2 * e + 1]) : 0;
+            const int u = (c + NT - 1) / NT;
+            int sum = u << 16 | c;  // both sums at once: at most 2048 rows and 1088 units
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, sum, o);
+                sum += lane >= o ? up : 0;
+            }
+            const int first = row0 + (sum & 0xFFFF) - c, unit = unit0 + (sum >> 16) - u;
+            if (e < E)
+                base[e] = uint16_t(first);
+            for (int i = 0; i < u; ++i)
+                units[unit + i] = FewUnit::pack(e, first + i * NT, min(NT, c - i * NT));
+            const int all = __shfl_sync(0xffffffffu, sum, 31);
+            row0 += all & 0xFFFF;
+            unit0 += all >> 16;
+        }
+        return unit0;
+    }
+};
 
 __device__ __forceinline__ uint2 bf16x4(float4 v)
 {
@@ -209,35 +212,42 @@ __device__ __forceinline__ void few_store_h(const FewArgs &a, int row, int tile,
         a.hs[size_t(tile) * (a.T * a.k) + row] = sc;
 }
 
-// The pair's product goes to memory; the warp that brings a token's last one adds them
+// The row's product goes to memory; the warp that brings a token's last one adds them
 // all, in the order of the choices.
-__device__ __forceinline__ void few_combine(const FewArgs &a, int pair, int tile, int lane, float4 v)
+__device__ __forceinline__ void few_combine(const FewArgs &a, const FewPlan &p, int row, int tile,
+                                            int lane, float4 v)
 {
-    const int t = pair / a.k;
+    const int t = p.token[row];
     const size_t col = size_t(tile) * 128 + 4 * lane;
+    *reinterpret_cast<float4 *>(a.part + size_t(row) * a.N + col) = v;
     const int id = few_choice(a, t, lane);
     const float weight = lane < a.k ? a.weights[t * a.k + lane] : 0.0f;
-    *reinterpret_cast<float4 *>(a.part + size_t(pair) * a.N + col) = v;
+    // choices that name the same expert share its row
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
     const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+    const uint32_t rows = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
     __threadfence();
     __syncwarp();
     int done = 0;
     if (lane == 0)
         done = atomicAdd(&a.count[t * (a.N / 128) + tile], 1) + 1;
     done = __shfl_sync(0xffffffffu, done, 0);
-    if (done != __popc(live))
+    if (done != __popc(rows))
         return;
     __threadfence();
+    const int at = id >= 0 ? p.row(id, t) : 0;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
         const float w = __shfl_sync(0xffffffffu, weight, j);
+        const int r = __shfl_sync(0xffffffffu, at, j);
         if (!((live >> j) & 1u))
             continue;
-        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part + size_t(t * a.k + j) * a.N + col));
-        y.x = fmaf(w, p.x, y.x);
-        y.y = fmaf(w, p.y, y.y);
-        y.z = fmaf(w, p.z, y.z);
-        y.w = fmaf(w, p.w, y.w);
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(a.part + size_t(r) * a.N + col));
+        y.x = fmaf(w, q.x, y.x);
+        y.y = fmaf(w, q.y, y.y);
+        y.z = fmaf(w, q.z, y.z);
+        y.w = fmaf(w, q.w, y.w);
     }
     few_store(a, t, tile, lane, y);
 }
@@ -288,12 +298,6 @@ __device__ __forceinline__ void few_quant(const uint4 (&v)[P], int r0, int rows,
     }
 }
 
-// The 128 threads of the promotion warps.
-__device__ __forceinline__ void promo_sync()
-{
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
 few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
@@ -306,21 +310,21 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *red = reinterpret_cast<float *>(smem + Cfg::RED_OFF);
     float *xs = reinterpret_cast<float *>(smem + Cfg::XS_OFF);
-    uint32_t *units = reinterpret_cast<uint32_t *>(smem + Cfg::UNIT_OFF);
-    int16_t *order = reinterpret_cast<int16_t *>(smem + Cfg::ORDER_OFF);
+    const FewPlan plan = {reinterpret_cast<uint32_t *>(smem + Cfg::MASK_OFF),
+                          reinterpret_cast<uint16_t *>(smem + Cfg::BASE_OFF),
+                          reinterpret_cast<uint32_t *>(smem + Cfg::UNIT_OFF), smem + Cfg::TOKEN_OFF};
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + NBUF;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + NBUF);
+    uint64_t *rfull = tempty + NBUF, *rempty = rfull + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rempty + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     __shared__ int unit_count;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = int(cluster_ctarank()), split = int(cluster_nctarank());
-    // the plan's scratch: the pairs' ids, and a count per expert
-    int *count = reinterpret_cast<int *>(red);
-    int16_t *id = reinterpret_cast<int16_t *>(red + 1024);
+    int16_t *id = reinterpret_cast<int16_t *>(red);  // scratch of the plan: the pairs' ids
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -331,13 +335,15 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 4);
         }
+        mbar_init(rfull, 4);
+        mbar_init(rempty, Cfg::EXPERTS ? Cfg::FIN_WARPS : 1);
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmW);
     }
     if (Cfg::EXPERTS)
-        for (int e = tid; e < a.E; e += Cfg::THREADS)
-            count[e] = 0;
+        for (int i = tid; i < 2 * a.E; i += Cfg::THREADS)
+            plan.mask[i] = 0;
     if (warp == 5) {
         tmem_alloc<1>(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish<1>();
@@ -356,6 +362,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     // down, codes: the kernel before this one (up; the quantizer) waited for its own
     // predecessor before it let this one start, so the ids and the weights are complete
     // and only what that kernel writes has to be waited for
+    if (Cfg::QUANT) {
+        // The tokens on their way to L2 before the weights take the memory's queues, a
+        // line for each thread of the grid (what that does not reach is loaded later).
+        const int64_t line = int64_t(blockIdx.x) * Cfg::THREADS + tid;
+        if (line < int64_t(a.T) * a.K / 64)
+            prefetch_l2(a.x + line * 64);
+    }
     if (KIND == FEW_UP)
         for (int i = int(blockIdx.x) * Cfg::THREADS + tid; i < a.T * a.tiles_h;
              i += int(gridDim.x) * Cfg::THREADS)
@@ -364,15 +377,15 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     int items = tiles;
     if (Cfg::EXPERTS) {
         for (int i = tid; i < a.T * a.k; i += Cfg::THREADS) {
-            const int v = a.ids[i];
+            const int v = a.ids[i], t = i / a.k;
             const bool ok = v >= 0 && v < a.E;
             id[i] = int16_t(ok ? v : -1);
             if (ok)
-                atomicAdd(&count[v], 1);
+                atomicOr(&plan.mask[2 * v + (t >> 5)], 1u << (t & 31));
         }
         __syncthreads();
         if (warp == 4) {
-            const int n = few_units<NT>(count, a.E, units, lane);
+            const int n = plan.make_units<NT>(a.E, lane);
             if (lane == 0)
                 unit_count = n;
         }
@@ -395,7 +408,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         w.tile = item;
         if (Cfg::EXPERTS && item < items) {
             const int unit = item / tiles;
-            w.u = FewUnit::of(units[unit]);
+            w.u = FewUnit::of(plan.units[unit]);
             w.tile = item - unit * tiles;
         }
     };
@@ -414,13 +427,16 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     };
     // MMA columns in use: whole groups of 16
     const auto columns = [](int rows) { return NT <= 16 ? 16 : (rows + 15) / 16 * 16; };
+    // Weights are read once: they must not push out of L2 what every item needs (codes,
+    // scales, the kernel's own code, which then comes from HBM behind them).
+    const uint64_t once = l2_evict_first();
     const auto load_weights = [&](const Walk &w, int s) {
         const int row = w.u.expert * a.N + w.tile * 128;
         uint8_t *dst = smem + s * Cfg::STAGE_BYTES;
         mbar_arrive_expect_tx(&full[s], Cfg::W_BYTES + (Cfg::QUANT ? 0 : Cfg::X_BYTES));
-        tma_load_2d(dst, &tmW, &full[s], (lo + w.i) * 128, row);
+        tma_load_2d_hint(dst, &tmW, &full[s], (lo + w.i) * 128, row, once);
         if (KIND == FEW_UP)
-            tma_load_2d(dst + 128 * 128, &tmW, &full[s], (lo + w.i) * 128, row + a.N / 2);
+            tma_load_2d_hint(dst + 128 * 128, &tmW, &full[s], (lo + w.i) * 128, row + a.N / 2, once);
     };
     // weights do not wait for the order of the rows, nor for the kernel before
     const int early = min(STAGES, blocks);
@@ -430,49 +446,60 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             load_weights(w, n);
     }
     if (Cfg::EXPERTS) {
-        if (warp == 0)
-            few_order(id, a.T * a.k, count, order, lane);
+        for (int i = tid; i < a.T * a.k; i += Cfg::THREADS)
+            if (id[i] >= 0)
+                plan.token[plan.row(id[i], i / a.k)] = uint8_t(i / a.k);
         __syncthreads();
     }
 
     if (warp < 4) {
         // ------------------------------------------------------------- promotion
-        Walk at;
-        for (int n = 0, item = first; n < blocks; item += step) {
-            enter(at, item);
-            const FewUnit u = at.u;
-            const int tile = at.tile, cols = columns(u.rows);
-            float2 acc[RT][NT / 2];
-            const float *sw[RT];
-            float next[RT];
+        Walk at, to;
+        enter(at, first);
+        const float *sw[RT];  // weight scales, loaded a block ahead, across items too
+        float next[RT];
+        const auto scales_of = [&](const Walk &w) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < RT; ++r)
+                sw[r] = a.sw + (size_t(w.u.expert) * n_tiles + w.tile + r * tiles) * a.KB + lo;
+        };
+        if (blocks > 0) {
+            scales_of(at);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                next[r] = __ldg(sw[r]);
+        }
+        bool ok = true;
+        for (int n = 0, m = 0; n < blocks && ok; at = to, ++m) {
+            const FewUnit u = at.u;
+            const int cols = columns(u.rows);
+            enter(to, at.item + step);
+            float2 acc[RT][NT / 2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int c = 0; c < NT / 2; ++c)
                     acc[r][c] = make_float2(0.0f, 0.0f);
-                sw[r] = a.sw + (size_t(u.expert) * n_tiles + tile + r * tiles) * a.KB + lo;
-                next[r] = __ldg(sw[r]);
-            }
             for (int i = 0; i < nkb; ++i, ++n) {
                 const int s = n % STAGES, b = n % NBUF;
                 float2 cur[RT];
+                const bool more = i + 1 < nkb;
+                if (!more && n + 1 < blocks)
+                    scales_of(to);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     cur[r] = make_float2(next[r], next[r]);
-                    if (i + 1 < nkb)
-                        next[r] = __ldg(sw[r] + i + 1);
+                    if (n + 1 < blocks)
+                        next[r] = __ldg(sw[r] + (more ? i + 1 : 0));
                 }
-                // The stage's full barrier cannot run ahead: it waits for this warp below.
-                // After a wait that ran out the blocks are gone through without waiting, so
-                // that the warps meet at their barriers all the same.
-                const bool ok =
-                    !*abort_flag &&
-                    mbar_wait_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
-                                      FERR_PROMO, FEW_WAIT_NS) &&
-                    mbar_wait_bounded(&tfull[b], uint32_t(n / NBUF) & 1u, abort_flag, &g_few_error,
-                                      FERR_PROMO, FEW_WAIT_NS);
-                if (!__all_sync(0xffffffffu, ok))
-                    continue;
+                // the stage's full barrier cannot run ahead: it waits for this warp below
+                ok = mbar_wait_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
+                                       FERR_PROMO, FEW_WAIT_NS) &&
+                     mbar_wait_bounded(&tfull[b], uint32_t(n / NBUF) & 1u, abort_flag, &g_few_error,
+                                       FERR_PROMO, FEW_WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
                 tc_fence_after();
                 const uint32_t taddr =
                     tmem_base + (uint32_t(warp * 32) << 16) + uint32_t(b * RT * NT);
@@ -509,7 +536,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                     mbar_arrive(&empty[s]);
                 }
             }
-            if (split > 1) {
+            if (!Cfg::EXPERTS || split > 1) {
                 // The only item: every product of this CTA is done (the last buffer was
                 // full), so the stages are free to take its parts, [RT][NT][128].
                 float *part = reinterpret_cast<float *>(smem);
@@ -524,6 +551,11 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                     }
                 continue;
             }
+            ok = ok && __all_sync(0xffffffffu,
+                                  mbar_wait_bounded(rempty, (uint32_t(m) & 1u) ^ 1u, abort_flag,
+                                                    &g_few_error, FERR_PROMO, FEW_WAIT_NS));
+            if (!ok)
+                break;
 #pragma unroll
             for (int c = 0; c < NT; c += 2) {
                 float2 v = acc[0][c / 2];
@@ -536,17 +568,9 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 if (c + 1 < u.rows)
                     red[(c + 1) * 128 + tid] = v.y;
             }
-            promo_sync();
-            for (int r = warp; r < u.rows; r += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(red + r * 128 + 4 * lane);
-                if (KIND == FEW_UP)
-                    few_store_h(a, u.base + r, tile, lane, v);
-                else if (KIND == FEW_DOWN)
-                    few_combine(a, order[u.base + r], tile, lane, v);
-                else
-                    few_store(a, r, tile, lane, v);
-            }
-            promo_sync();  // the next item's sums may take their place
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(rfull);
         }
     } else if (warp == 4) {
         // -------------------------------------------------------------- producer
@@ -569,12 +593,18 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                                 (lo + w.i) * 128, w.u.base);
             }
         }
-    } else if (warp == 5) {
+    } else if (warp < Cfg::ACT_WARP0) {
         // ------------------------------------------------------------------- MMA
         if (lane == 0) {
-            Walk w = start(0);
-            for (int n = 0; n < blocks; ++n, advance(w, 1)) {
-                const int s = n % STAGES, b = n % NBUF;
+            static_assert(NBUF == 2, "one MMA warp per buffer");
+            const int b = warp - 5;
+            Walk w = {};
+            if (b < blocks) {
+                w = start(0);
+                advance(w, b);
+            }
+            for (int n = b; n < blocks; n += NBUF, advance(w, NBUF)) {
+                const int s = n % STAGES;
                 const uint32_t idesc = make_idesc_e4m3(128, columns(w.u.rows), 0);
                 if (!mbar_spin_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
                                        FERR_MMA_FULL, FEW_WAIT_NS) ||
@@ -595,6 +625,28 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 mma_commit(&tfull[b]);
             }
         }
+    } else if (Cfg::EXPERTS && warp >= Cfg::FIN_WARP0) {
+        // --------------------------------------------------------- finish the rows
+        Walk at;
+        for (int n = 0, item = first, m = 0; n < blocks && split == 1; n += nkb, item += step, ++m) {
+            enter(at, item);
+            const bool ok = mbar_wait_bounded(rfull, uint32_t(m) & 1u, abort_flag, &g_few_error,
+                                              FERR_FINISH, FEW_WAIT_NS);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            for (int r = warp - Cfg::FIN_WARP0; r < at.u.rows; r += Cfg::FIN_WARPS) {
+                const float4 v = *reinterpret_cast<const float4 *>(red + r * 128 + 4 * lane);
+                if (KIND == FEW_UP)
+                    few_store_h(a, at.u.base + r, at.tile, lane, v);
+                else if (KIND == FEW_DOWN)
+                    few_combine(a, plan, at.u.base + r, at.tile, lane, v);
+                else
+                    few_store(a, r, at.tile, lane, v);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(rempty);
+        }
     } else if (Cfg::QUANT) {
         // -------------------------------------------- quantize the tokens' groups
         // One block per warp in turn; four row pairs at a time, the next four's values under
@@ -607,7 +659,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 const int r = r0 + 2 * q + (lane >> 4);
                 v[q] = make_uint4(0u, 0u, 0u, 0u);
                 if (w.item < items && r < w.u.rows) {
-                    const int t = KIND == FEW_UP ? int(order[w.u.base + r]) / a.k : r;
+                    const int t = KIND == FEW_UP ? int(plan.token[w.u.base + r]) : r;
                     v[q] = __ldg(x4 + (t * (a.K / 8) + w.i * 16));
                 }
             }
@@ -616,10 +668,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         Walk w = {}, next;
         if (blocks > 0) {
             w = start(0);
-            advance(w, warp - 6);
+            advance(w, warp - Cfg::ACT_WARP0);
             fetch(w, 0, v);
         }
-        for (int n = warp - 6; n < blocks; n += Cfg::ACT_WARPS, w = next) {
+        for (int n = warp - Cfg::ACT_WARP0; n < blocks; n += Cfg::ACT_WARPS, w = next) {
             const int s = n % STAGES, rows = w.u.rows;
             next = w;
             advance(next, Cfg::ACT_WARPS);
@@ -679,9 +731,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         tc_fence_after();
         tmem_dealloc<1>(tmem_base, Cfg::TMEM_COLS);
     }
-    if (split > 1) {
+    if (!Cfg::EXPERTS || split > 1) {
         // ---------------------------------------------------- join the cluster's parts
-        cluster_sync();
+        if (split > 1)
+            cluster_sync();
         if (first < items) {
             Walk w;
             enter(w, first);
@@ -713,12 +766,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                                 make_float4(swiglu(g.x, up.x), swiglu(g.y, up.y), swiglu(g.z, up.z),
                                             swiglu(g.w, up.w)));
                 else if (KIND == FEW_DOWN)
-                    few_combine(a, order[u.base + r], tile, lane, g);
+                    few_combine(a, plan, u.base + r, tile, lane, g);
                 else
                     few_store(a, r, tile, lane, g);
             }
         }
-        cluster_sync();  // no peer reads this CTA's parts any more
+        if (split > 1)
+            cluster_sync();  // no peer reads this CTA's parts any more
     }
     if (KIND == FEW_DOWN)
         // tokens that chose no expert: one warp for each of their tiles
@@ -766,10 +820,11 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
     th = tw;  // only used where the tokens' codes are in memory
     if (!Cfg::QUANT && !codes_map(&th, codes, uint64_t(a.sx_rows), uint64_t(a.K), Cfg::NT))
         return cudaErrorInvalidValue;
-    // The most items there may be: an expert's rows make whole units but for one.  A
-    // cluster takes one item at most, so those that split theirs have to cover them all.
-    const int64_t pairs = int64_t(a.T) * a.k;
-    const int64_t units = Cfg::EXPERTS ? (pairs < a.E ? pairs : a.E) + pairs / Cfg::NT : 1;
+    // The most items there may be: an expert's rows make whole units but for one, which
+    // is the only one where all tokens make no more.  A cluster takes one item at most, so
+    // those that split theirs have to cover them all.
+    const int64_t pairs = int64_t(a.T) * a.k, whole = a.T <= Cfg::NT ? 0 : pairs / Cfg::NT;
+    const int64_t units = Cfg::EXPERTS ? (pairs < a.E ? pairs : a.E) + whole : 1;
     const int64_t items = units * (a.N / 128 / Cfg::RT), slots = int64_t(num_sms) * Cfg::BLOCKS;
     const int split = few_split(items, a.KB, slots);
     cudaLaunchConfig_t cfg = {};
@@ -779,7 +834,8 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
     at[1].val.clusterDim.x = unsigned(split);
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(split > 1 || items < slots ? items * split : slots));
+    // an expert CTA walks items; the others have one each
+    cfg.gridDim = dim3(unsigned(!Cfg::EXPERTS || split > 1 || items < slots ? items * split : slots));
     cfg.blockDim = dim3(Cfg::THREADS);
     cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = stream;

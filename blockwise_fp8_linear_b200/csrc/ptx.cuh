@@ -117,16 +117,16 @@ __device__ __forceinline__ bool mbar_spin_bounded(uint64_t *bar, uint32_t parity
                                                   volatile int *abort, int *err, int code,
                                                   uint64_t limit_ns)
 {
-    if (mbar_test_wait(bar, parity))
-        return true;
-    uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;  // read after the first 256 tests: a short wait does without the timer
     for (uint32_t it = 1;; ++it) {
         if (mbar_test_wait(bar, parity))
             return true;
         if ((it & 255u) == 0) {
             if (*abort)
                 return false;
-            if (global_timer_ns() - t0 > limit_ns) {
+            if (t0 == 0) {
+                t0 = global_timer_ns();
+            } else if (global_timer_ns() - t0 > limit_ns) {
                 atomicCAS(err, 0, code);
                 *abort = 1;
                 return false;
@@ -256,6 +256,31 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
         : "memory");
+}
+
+// An L2 policy for data that is read once: it makes room first.
+__device__ __forceinline__ uint64_t l2_evict_first()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// tma_load_2d with an L2 policy.
+__device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                                 int32_t c0, int32_t c1, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "l"(policy)
+        : "memory");
+}
+
+// Ask for the 128-byte line of `p` to be brought to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
 // -------------------------------------------------------------- cp.async (LDGSTS)

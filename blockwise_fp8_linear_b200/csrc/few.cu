@@ -12,7 +12,7 @@
 // tcgen05.mma takes a whole 128 x 32 weight tile and TMA streams weights straight into
 // shared memory without passing through registers.  An item of work is a tile of 128
 // weight rows (up: 128 gate rows and the 128 up rows beside them) for the tokens of one
-// expert.  The experts' CTAs, one to an SM, walk the items; loads and products of the next item run
+// expert.  The experts' CTAs walk the items; loads and products of the next item run
 // while one is finished.  Where the items are fewer than the SMs, the CTAs of a cluster
 // split the reduction of one item between them and join their FP32 sums through
 // distributed shared memory in a fixed order.
@@ -83,10 +83,13 @@ struct FewCfg {
     static constexpr int W_BYTES = RT * 128 * 128;
     static constexpr int X_BYTES = NT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    // The linear's CTAs have one item each and share an SM with the next kernel's.
-    static constexpr int BLOCKS = EXPERTS ? 1 : 2;
+    // CTAs per SM: one with a deep ring where many items stream through it; two where a
+    // few items' latency counts, so that one's start runs under the other's loads (and
+    // down's under up's).
+    static constexpr int BLOCKS = EXPERTS && NT > 16 ? 1 : 2;
     static constexpr int ACT_WARP0 = 7;
     static constexpr int ACT_WARPS = KIND == FEW_LINEAR ? 4 : KIND == FEW_UP ? 2 : 1;
+    static constexpr int ROW_PAIRS = KIND == FEW_UP && BLOCKS == 2 ? 2 : 4;  // quantized at a time
     static constexpr int FIN_WARP0 = ACT_WARP0 + ACT_WARPS;
     // (up has three: 12 warps leave its promotion warps the registers for their sums)
     static constexpr int FIN_WARPS = KIND == FEW_UP ? 3 : KIND == FEW_DOWN ? 4 : 0;
@@ -504,28 +507,27 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 const uint32_t taddr =
                     tmem_base + (uint32_t(warp * 32) << 16) + uint32_t(b * RT * NT);
                 const float4 *xs4 = reinterpret_cast<const float4 *>(xs + s * NT);
-                // 16 columns at a time: the sums already take RT x NT registers
+                // 16 columns of one tile at a time: the sums already take RT x NT registers
 #pragma unroll
                 for (int c0 = 0; c0 < NT; c0 += 16) {
-                    if (c0 < cols) {
-                        uint32_t v[RT][16];
+                    if (c0 >= cols)
+                        break;
 #pragma unroll
-                        for (int r = 0; r < RT; ++r)
-                            tmem_ld_32x32b_x16(taddr + uint32_t(r * NT + c0), v[r]);
+                    for (int r = 0; r < RT; ++r) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(taddr + uint32_t(r * NT + c0), v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
                             const float4 x4 = xs4[(c0 + c) / 4];
                             const float2 xc[2] = {make_float2(x4.x, x4.y), make_float2(x4.z, x4.w)};
 #pragma unroll
-                            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    float2 &o = acc[r][(c0 + c) / 2 + q];
-                                    o = __ffma2_rn(make_float2(__uint_as_float(v[r][c + 2 * q]),
-                                                               __uint_as_float(v[r][c + 2 * q + 1])),
-                                                   __fmul2_rn(cur[r], xc[q]), o);
-                                }
+                            for (int q = 0; q < 2; ++q) {
+                                float2 &o = acc[r][(c0 + c) / 2 + q];
+                                o = __ffma2_rn(make_float2(__uint_as_float(v[c + 2 * q]),
+                                                           __uint_as_float(v[c + 2 * q + 1])),
+                                               __fmul2_rn(cur[r], xc[q]), o);
+                            }
                         }
                     }
                 }
@@ -649,9 +651,9 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         }
     } else if (Cfg::QUANT) {
         // -------------------------------------------- quantize the tokens' groups
-        // One block per warp in turn; four row pairs at a time, the next four's values under
+        // One block per warp in turn, a few row pairs at a time, the next ones' values under
         // way meanwhile.
-        constexpr int P = 4;
+        constexpr int P = Cfg::ROW_PAIRS;
         const uint4 *x4 = reinterpret_cast<const uint4 *>(a.x) + lo * 16 + (lane & 15);
         const auto fetch = [&](const Walk &w, int r0, uint4 (&v)[P]) {
 #pragma unroll

@@ -377,7 +377,7 @@ int64_t fp8_moe_plan_rows(int64_t T, int64_t E, int64_t k)
 
 int64_t fp8_moe_plan_workspace(int64_t T, int64_t E, int64_t k)
 {
-    return plan_ok(T, E, k) ? int64_t(fp8bw::moe_plan_workspace(T, int(k), int(E))) : 0;
+    return plan_ok(T, E, k) ? int64_t(fp8bw::moe_plan_workspace(int(E))) : 0;
 }
 
 int fp8_moe_plan(const int32_t *ids, int64_t T, int64_t E, int64_t k, int32_t *seg, int32_t *row,

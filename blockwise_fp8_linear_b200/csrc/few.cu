@@ -226,8 +226,8 @@ __device__ __forceinline__ void few_combine(const FewArgs &a, const FewPlan &p, 
     const int id = few_choice(a, t, lane);
     const float weight = lane < a.k ? a.weights[t * a.k + lane] : 0.0f;
     // choices that name the same expert share its row
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
     const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+    const uint32_t same = same_key(uint32_t(id), 32 - __clz(a.E - 1)) & live;
     const uint32_t rows = __ballot_sync(0xffffffffu, id >= 0 && __ffs(same) - 1 == lane);
     __threadfence();
     __syncwarp();

@@ -17,7 +17,7 @@ cudaError_t launch_moe_route_bwd(const float *dweights, const float *weights, co
 
 // Plan: the (token, choice) pairs laid out by expert in blocks of 128 rows.
 int64_t moe_plan_rows(int64_t T, int k, int E);
-size_t moe_plan_workspace(int64_t T, int k, int E);
+size_t moe_plan_workspace(int E);
 cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t *seg,
                             int32_t *row, int32_t *src, void *workspace, cudaStream_t stream);
 

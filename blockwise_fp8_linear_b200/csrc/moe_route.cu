@@ -26,33 +26,100 @@ template <class T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
-// A logit that may be chosen: finite.  +inf counts as the largest finite value, so that
-// the softmax stays defined; -inf and NaN mark experts that are not available (-inf here).
-__device__ __forceinline__ float usable(float v)
+// A logit that may be chosen: finite.  +inf counts as the type's largest finite value, so
+// that the softmax stays defined; -inf and NaN mark experts that are not available (-inf
+// here).
+template <class T> __device__ __forceinline__ float usable(float v)
 {
-    return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;
+    const float most = sizeof(T) == 2 ? __uint_as_float(0x7F7F0000u) : FLT_MAX;
+    return v > -INFINITY ? fminf(v, most) : -INFINITY;
 }
 
-template <class T, int V, int NV>
-__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&v)[NV])
+// Rows with +inf or NaN among their logits are rare: one vote finds them, and only they
+// pay for usable() (-inf goes its way without).
+template <class T, int NV> __device__ __forceinline__ void make_usable(float (&v)[NV])
 {
-    struct alignas(sizeof(T) * V) Vec { T e[V]; };
+    bool plain = true;
 #pragma unroll
-    for (int c = 0; c < NV / V; ++c) {
-        const int at = (c * 32 + lane) * V;
-        if (at < E) {  // E is a multiple of V
-            const Vec w = *reinterpret_cast<const Vec *>(row + at);
+    for (int i = 0; i < NV; ++i)
+        plain = plain && v[i] < INFINITY;
+    if (!__all_sync(0xffffffffu, plain)) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[c * V + i] = usable(to_f32(w.e[i]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[c * V + i] = -INFINITY;
-        }
+        for (int i = 0; i < NV; ++i)
+            v[i] = usable<T>(v[i]);
     }
 }
 
+// V neighbouring logits in one load: one of them, or 16 bytes.
+template <class T, int V> struct Piece;
+template <class T> struct Piece<T, 1> {
+    T e;
+    __device__ __forceinline__ float get(int) const { return to_f32(e); }
+    __device__ __forceinline__ static Piece pack(const float *v) { return {from_f32<T>(v[0])}; }
+};
+template <> struct Piece<float, 4> {
+    float4 e;
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? e.x : i == 1 ? e.y : i == 2 ? e.z : e.w; }
+    __device__ __forceinline__ static Piece pack(const float *v) { return {make_float4(v[0], v[1], v[2], v[3])}; }
+};
+template <> struct Piece<__nv_bfloat16, 8> {
+    uint4 e;
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w = i < 2 ? e.x : i < 4 ? e.y : i < 6 ? e.z : e.w;
+        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+    __device__ __forceinline__ static Piece pack(const float *v)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return {make_uint4(w[0], w[1], w[2], w[3])};
+    }
+};
+
+// The row as it is loaded (so that the next row's can be under way) and its values.
+template <class T, int V, int NV> struct Row {
+    Piece<T, V> raw[NV / V];
+    __device__ __forceinline__ void load(const T *row, int E, int lane)
+    {
+#pragma unroll
+        for (int c = 0; c < NV / V; ++c) {
+            const int at = (c * 32 + lane) * V;
+            if (at < E)  // E is a multiple of V
+                raw[c] = *reinterpret_cast<const Piece<T, V> *>(row + at);
+        }
+    }
+    __device__ __forceinline__ void values(int E, int lane, float (&v)[NV]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] = (i / V * 32 + lane) * V < E ? raw[i / V].get(i % V) : -INFINITY;
+    }
+    __device__ __forceinline__ static void copy(T *to, const T *from, int E, int lane)
+    {
+#pragma unroll
+        for (int c = 0; c < NV / V; ++c) {
+            const int at = (c * 32 + lane) * V;
+            if (at < E)
+                *reinterpret_cast<Piece<T, V> *>(to + at) = *reinterpret_cast<const Piece<T, V> *>(from + at);
+        }
+    }
+    __device__ __forceinline__ static void store(T *row, int E, int lane, const float (&v)[NV])
+    {
+#pragma unroll
+        for (int c = 0; c < NV / V; ++c) {
+            const int at = (c * 32 + lane) * V;
+            if (at < E)
+                *reinterpret_cast<Piece<T, V> *>(row + at) = Piece<T, V>::pack(v + c * V);
+        }
+    }
+};
+
+// (register i of a lane is as many experts after its register 0 as in lane 0)
 template <int V> __device__ __forceinline__ int expert_of(int i, int lane)
 {
     return (i / V * 32 + lane) * V + i % V;
@@ -73,17 +140,96 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v)
+// The float of an order key other than 0.
+__device__ __forceinline__ float key_value(uint32_t key)
 {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    return __uint_as_float((key >> 31) ? (key ^ 0x80000000u) : ~key);
 }
 
+// exp(d) for d <= 0 by the hardware's base-2 exponential (2 ulp; the product's rounding
+// adds |d| 2^-24).  -inf gives 0.
+__device__ __forceinline__ float exp_neg(float d)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.44269504088896341f));
+    return r;
+}
+
+// What is left of a row, each lane's registers as in load_row: next() gives the largest
+// remaining logit and its expert, ties to the lowest, and takes it out; key 0 when none
+// is left.
+//
+// BF16 logits: value and expert fit one word, (16-bit order key, ~expert), so that words
+// are distinct and one warp-wide maximum (redux) finds both.  Nothing has to be taken
+// out: relative to the last maximum, counting down modulo 2^32, what is below it comes
+// before what is not.
+template <class T, int V, int NV> struct RowTop {
+    uint32_t word[NV], last;
+    __device__ __forceinline__ void init(const float (&v)[NV], int lane)
+    {
+        last = 0u;
+        const uint32_t first = 0xFFFFu - uint32_t(expert_of<V>(0, lane));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t u = __float_as_uint(__fadd_rn(v[i], 0.0f));
+            const uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+            word[i] = (key & 0xFFFF0000u) | (first - uint32_t(expert_of<V>(i, 0)));
+        }
+    }
+    // The next word, 0 when none is left (-inf has the lowest key, 0x007F).
+    __device__ __forceinline__ uint32_t next()
+    {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            best = max(best, word[i] - last);
+        last += __reduce_max_sync(0xffffffffu, best);
+        return last >= 0x00800000u ? last : 0u;
+    }
+    // (the low half of a BF16 value's key is all its sign's)
+    __device__ __forceinline__ static uint32_t key_of(uint32_t w)
+    {
+        return w == 0u ? 0u : (w >> 31) ? w & 0xFFFF0000u : w | 0xFFFFu;
+    }
+    __device__ __forceinline__ static int expert(uint32_t w) { return int(0xFFFFu - (w & 0xFFFFu)); }
+};
+
+// FP32 logits: a maximum of the values, then the lowest expert that has it.  A choice is
+// a 64-bit word, (key, ~expert).
+template <int V, int NV> struct RowTop<float, V, NV> {
+    uint32_t left[NV];
+    uint32_t first;  // expert of register 0
+    __device__ __forceinline__ void init(const float (&v)[NV], int lane)
+    {
+        first = uint32_t(expert_of<V>(0, lane));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            left[i] = order_key(v[i]);
+    }
+    __device__ __forceinline__ uint64_t next()
+    {
+        uint32_t best = left[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i)
+            best = max(best, left[i]);
+        const uint32_t key = __reduce_max_sync(0xffffffffu, best);
+        uint32_t mine = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i)
+            mine = left[i] == key ? first + uint32_t(expert_of<V>(i, 0)) : mine;
+        const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            left[i] = e - first == uint32_t(expert_of<V>(i, 0)) ? 0u : left[i];
+        return key ? uint64_t(key) << 32 | e : 0u;
+    }
+    __device__ __forceinline__ static uint32_t key_of(uint64_t w) { return uint32_t(w >> 32); }
+    __device__ __forceinline__ static int expert(uint64_t w) { return int(uint32_t(w)); }
+};
+
 // weights[t][j], ids[t][j] for the k largest logits of row t, largest first, ties to
-// the lowest expert.  One warp per token: k rounds of a warp-wide maximum (redux) over
-// each lane's best remaining value; lane j keeps choice j.  Statistics in FP32.
+// the lowest expert.  One warp per token, k rounds of RowTop; lane j keeps choice j.
+// Statistics in FP32.  Bound by issue slots: about 2 NV + 12 instructions a round.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int renorm,
@@ -92,65 +238,57 @@ moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int r
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5); t < rows;
-         t += int64_t(gridDim.x) * ROUTE_WARPS) {
+    const int64_t step = int64_t(gridDim.x) * ROUTE_WARPS;
+    int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5);
+    Row<T, V, NV> next;
+    if (t < rows)
+        next.load(logits + t * E, E, lane);
+    for (; t < rows; t += step) {
         float v[NV];
-        load_row<T, V, NV>(logits + t * E, E, lane, v);
-        uint32_t left[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            left[i] = order_key(v[i]);
-        float mine = -INFINITY, top = 0.0f;
-        int my_id = -1;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = left[0];
-            int at = 0;
-#pragma unroll
-            for (int i = 1; i < NV; ++i)
-                if (left[i] > best) {
-                    best = left[i];
-                    at = i;
-                }
-            const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-            if (high == 0u)  // nothing is left: this choice and the later ones stay empty
+        next.values(E, lane, v);
+        make_usable<T>(v);
+        if (t + step < rows)
+            next.load(logits + (t + step) * E, E, lane);
+        RowTop<T, V, NV> row;
+        row.init(v, lane);
+        auto mine = row.next();  // lane j: choice j, in the end
+        const auto top_word = mine;
+        int left = 1;  // choices there are
+        for (int j = 1; j < k; ++j) {
+            const auto w = row.next();
+            if (w == 0u)  // nothing is left: this choice and the later ones stay empty
                 break;
-            const uint32_t e = best == high ? uint32_t(expert_of<V>(at, lane)) : 0xFFFFFFFFu;
-            const uint32_t first = __reduce_min_sync(0xffffffffu, e);
+            mine = lane >= j ? w : mine;
+            left = j + 1;
+        }
+        const uint32_t top_key = row.key_of(top_word);
+        const uint32_t my_key = lane < left ? row.key_of(mine) : 0u;
+        const int my_id = my_key ? row.expert(mine) : -1;
+        const float top = key_value(top_key);
+        const float p = my_key ? exp_neg(key_value(my_key) - top) : 0.0f;
+        float s = p;
+        if (!renorm) {
+            s = 0.0f;
+            if (top_key) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (first == uint32_t(expert_of<V>(i, lane)))
-                    left[i] = 0u;
-            const uint32_t u = (high >> 31) ? (high ^ 0x80000000u) : ~high;
-            const float val = __uint_as_float(u);
-            if (j == 0)
-                top = val;
-            if (lane == j) {
-                mine = val;
-                my_id = int(first);
+                for (int i = 0; i < NV; ++i)
+                    s += exp_neg(v[i] - top);
             }
         }
-        const float p = my_id >= 0 ? expf(mine - top) : 0.0f;
-        float den;
-        if (renorm) {
-            den = warp_sum(p);
-        } else {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                s += v[i] > -INFINITY ? expf(v[i] - top) : 0.0f;
-            den = warp_sum(s);
-        }
+        const float den = warp_sum(s);
         if (lane < k) {
-            weights[t * k + lane] = my_id >= 0 ? p / den : 0.0f;
+            weights[t * k + lane] = my_key ? p / den : 0.0f;
             ids[t * k + lane] = my_id;
         }
     }
 }
 
-// dlogits = direct - p * (sum_j w_j dw_j): direct is w_j dw_j at the chosen experts, p
-// the softmax over the chosen experts (renorm, so p = w there and 0 elsewhere) or over
-// all.  Every element of the row is written.  A choice with an id outside [0, E) takes
-// no part.  One warp per token, in FP32, rounded once to the logits' type.
+// dlogits = direct - p * G with G = sum_j w_j dw_j: direct is w_j dw_j at the chosen
+// experts, p the softmax over the chosen experts (renorm) or over all; at a chosen
+// expert p is its weight, so that the element is w_j (dw_j - G).  Every element of the row
+// is written, first the row without its choices, then these.  A choice with an id
+// outside [0, E) takes no part.  One warp per token, in FP32, rounded once to the logits'
+// type.  Bound by HBM: the row written, and read for the softmax over all.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict__ weights,
@@ -160,137 +298,183 @@ moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5); t < rows;
-         t += int64_t(gridDim.x) * ROUTE_WARPS) {
-        int id = -1;
-        float w = 0.0f, dw = 0.0f;
+    // the row is put together in shared memory: single elements stored over it in global
+    // memory would cost a sector each
+    __shared__ __align__(16) T rows_out[ROUTE_WARPS][NV * 32];
+    __shared__ uint8_t lanes_out[ROUTE_WARPS][NV * 32];
+    T *out = rows_out[threadIdx.x >> 5];
+    uint8_t *out_lane = lanes_out[threadIdx.x >> 5];
+    const int64_t step = int64_t(gridDim.x) * ROUTE_WARPS;
+    int64_t t = int64_t(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5);
+    // the next row's inputs are under way while a row is worked on
+    Row<T, V, NV> next;
+    int next_id = -1;
+    float next_w = 0.0f, next_dw = 0.0f;
+    const auto fetch = [&](int64_t at) {
+        if (at >= rows)
+            return;
+        if (!renorm)
+            next.load(logits + at * E, E, lane);
         if (lane < k) {
-            id = ids[t * k + lane];
-            w = weights[t * k + lane];
-            dw = dweights[t * k + lane];
+            next_id = ids[at * k + lane];
+            next_w = weights[at * k + lane];
+            next_dw = dweights[at * k + lane];
         }
-        const bool some = id >= 0 && id < E;
-        const float direct = some ? w * dw : 0.0f;
-        const float total = warp_sum(direct);
-        const float g = renorm ? direct - (some ? w : 0.0f) * total : direct;
+    };
+    fetch(t);
+    for (; t < rows; t += step) {
+        const int id = next_id;
+        const float w = next_w, dw = next_dw;
         float d[NV];
+        if (!renorm) {
+            next.values(E, lane, d);
+            make_usable<T>(d);
+        }
+        fetch(t + step);
+        const bool some = id >= 0 && id < E;
+        const float total = warp_sum(some ? w * dw : 0.0f);
+        float g = w * (dw - total);
         if (renorm) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 d[i] = 0.0f;
         } else {
-            load_row<T, V, NV>(logits + t * E, E, lane, d);
-            float m = -INFINITY;
+            // p = w0 exp(l - l0), from the weight and the logit of the first choice
+            const int id0 = __shfl_sync(0xffffffffu, some ? id : -1, 0);
+            const float w0 = __shfl_sync(0xffffffffu, w, 0);
+            float top = 0.0f, c = 0.0f;
+            if (id0 >= 0) {
+                float mine = d[0];
+#pragma unroll
+                for (int i = 1; i < NV; ++i)
+                    mine = id0 - expert_of<V>(0, lane) == expert_of<V>(i, 0) ? d[i] : mine;
+                top = __shfl_sync(0xffffffffu, mine, id0 / V & 31);
+                c = -total * w0;
+            } else {
+                // left out: the softmax anew
+                float m = d[0], s = 0.0f;
+#pragma unroll
+                for (int i = 1; i < NV; ++i)
+                    m = fmaxf(m, d[i]);
+                const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(m));
+                top = key ? key_value(key) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    s += exp_neg(d[i] - top);
+                s = warp_sum(s);
+                c = s > 0.0f ? -total / s : 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                m = fmaxf(m, d[i]);
-            m = warp_max(m);
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                d[i] = d[i] > -INFINITY ? expf(d[i] - m) : 0.0f;
-                s += d[i];
-            }
-            s = warp_sum(s);
-            const float c = s > 0.0f ? -total / s : 0.0f;
+                d[i] = exp_neg(d[i] - top);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 d[i] *= c;
         }
-        for (int j = 0; j < k; ++j) {
-            const int e = __shfl_sync(0xffffffffu, some ? id : -1, j);
-            const float ge = __shfl_sync(0xffffffffu, g, j);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e == expert_of<V>(i, lane))
-                    d[i] += ge;
-        }
-        struct alignas(sizeof(T) * V) Vec { T e[V]; };
-#pragma unroll
-        for (int c = 0; c < NV / V; ++c) {
-            const int at = (c * 32 + lane) * V;
-            if (at < E) {
-                Vec o;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o.e[i] = from_f32<T>(d[c * V + i]);
-                *reinterpret_cast<Vec *>(dlogits + t * E + at) = o;
+        __syncwarp();  // the last row has left the buffer
+        Row<T, V, NV>::store(out, E, lane, d);
+        // An expert named twice (never by the router) collects its choices in their order:
+        // the sum of w dw, less p G with p the weights' sum.
+        if (some)
+            out_lane[id] = uint8_t(lane);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, some && out_lane[id] != lane)) {
+            const uint32_t live = __ballot_sync(0xffffffffu, some);
+            const uint32_t same = same_key(uint32_t(id), 32 - __clz(E - 1)) & live;
+            float sum = 0.0f;
+            for (int j = 0; j < k; ++j) {
+                const float gj = __shfl_sync(0xffffffffu, g, j);
+                if ((same >> j) & 1u)
+                    sum += gj;
             }
+            g = sum;
         }
+        __syncwarp();  // the row comes first
+        if (some)
+            out[id] = from_f32<T>(g);
+        __syncwarp();
+        Row<T, V, NV>::copy(dlogits + t * E, out, E, lane);
     }
 }
 
 // ------------------------------------------------------------------------- plan
 
 // The pairs (t, j), in order p = t * k + j, are cut into `chunks` equal runs, one CTA
-// each, and each CTA's run into one run per warp.  Counting the ids of every run
-// gives, by prefix sums over warps and chunks, the place at which each run's first pair
-// of an expert goes; inside a run a warp ranks 32 pairs at a time by matching ids.  All
-// sums are of whole numbers, and a pair's place depends on the ids alone.
-constexpr int PLAN_WARPS = 16;
+// each, and each CTA's run into one run per warp, which keeps its ids in registers.
+// Counting the ids of every run gives, by prefix sums over warps and chunks, the place at
+// which each run's first pair of an expert goes; inside a run a warp ranks 32 pairs at a
+// time by matching ids.  All sums are of whole numbers, and a pair's place depends on the
+// ids alone.  Every CTA adds up all chunks' counts for itself, so there are few chunks.
+constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
 constexpr int PLAN_PAIRS = 2048;  // pairs of a chunk, at least
-constexpr int PLAN_CHUNKS = 128;
+constexpr int PLAN_CHUNKS = 64;
+constexpr int PLAN_REGS = 16;     // 32-pair steps of a warp's run, at most
 
 static int plan_chunks(int64_t pairs)
 {
     const int64_t c = (pairs + PLAN_PAIRS - 1) / PLAN_PAIRS;
     return int(c < 1 ? 1 : c > PLAN_CHUNKS ? PLAN_CHUNKS : c);
 }
+// (the layout holds at most 2^20 rows, and so pairs)
+static_assert(int64_t(PLAN_CHUNKS) * PLAN_WARPS * PLAN_REGS * 32 >= (1 << 20), "runs hold all pairs");
 
+// One warp's run: its ids, -1 outside [0, E) and behind the end.
 struct PlanRun {
-    int64_t lo, hi;
-    __device__ PlanRun(int64_t pairs, int chunk, int chunks, int warp)
+    int lo, hi;
+    int id[PLAN_REGS];
+    __device__ __forceinline__ void load(const int32_t *ids, int pairs, int E, int chunk, int chunks,
+                                         int warp, int lane)
     {
-        const int64_t runs = int64_t(chunks) * PLAN_WARPS, r = int64_t(chunk) * PLAN_WARPS + warp;
-        const int64_t len = ((pairs + runs - 1) / runs + 31) / 32 * 32;
-        lo = min(pairs, r * len);
+        const int runs = chunks * PLAN_WARPS, r = chunk * PLAN_WARPS + warp;
+        const int len = ((pairs + runs - 1) / runs + 31) / 32 * 32;
+        lo = int(min(int64_t(pairs), int64_t(r) * len));
         hi = min(pairs, lo + len);
+#pragma unroll
+        for (int i = 0; i < PLAN_REGS; ++i) {
+            const int p = lo + 32 * i + lane;
+            const int v = p < hi ? ids[p] : -1;
+            id[i] = v >= 0 && v < E ? v : -1;
+        }
+    }
+    // Adds them to cnt[E] (shared, this warp's own).
+    __device__ __forceinline__ void count(int *cnt) const
+    {
+#pragma unroll
+        for (int i = 0; i < PLAN_REGS; ++i)
+            if (id[i] >= 0)
+                atomicAdd(&cnt[id[i]], 1);
     }
 };
 
-// Adds each id of the warp's run to cnt[E] (shared, this warp's own); -1 for an id
-// outside [0, E).
-__device__ __forceinline__ void plan_count(const int32_t *ids, const PlanRun &run, int E, int lane,
-                                           int *cnt)
-{
-    for (int64_t p = run.lo + lane; p < run.hi; p += 32) {
-        const int id = ids[p];
-        if (id >= 0 && id < E)
-            atomicAdd(&cnt[id], 1);
-    }
-}
-
 __global__ void __launch_bounds__(PLAN_THREADS)
-moe_plan_count_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E, int *__restrict__ hist)
+moe_plan_count_kernel(const int32_t *__restrict__ ids, int pairs, int E, int *__restrict__ hist)
 {
-    extern __shared__ int cnt[];  // [PLAN_WARPS][E]
+    extern __shared__ int cnt[];  // [E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < PLAN_WARPS * E; i += PLAN_THREADS)
-        cnt[i] = 0;
+    for (int e = threadIdx.x; e < E; e += PLAN_THREADS)
+        cnt[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    plan_count(ids, PlanRun(pairs, blockIdx.x, gridDim.x, warp), E, lane, cnt + warp * E);
+    PlanRun run;
+    run.load(ids, pairs, E, blockIdx.x, gridDim.x, warp, lane);
+    run.count(cnt);
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
-        int s = 0;
-        for (int w = 0; w < PLAN_WARPS; ++w)
-            s += cnt[w * E + e];
-        hist[blockIdx.x * E + e] = s;
-    }
+    for (int e = threadIdx.x; e < E; e += PLAN_THREADS)
+        hist[e * PLAN_CHUNKS + blockIdx.x] = cnt[e];
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS)
-moe_plan_place_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
-                      const int *__restrict__ hist, int64_t rows, int32_t *__restrict__ seg,
+moe_plan_place_kernel(const int32_t *__restrict__ ids, int pairs, int E,
+                      const int *__restrict__ hist, int rows, int32_t *__restrict__ seg,
                       int32_t *__restrict__ row, int32_t *__restrict__ src)
 {
     extern __shared__ int sh[];
-    int *cnt = sh;                    // [PLAN_WARPS][E]
+    int *cnt = sh;                      // [PLAN_WARPS][E]
     int *total = cnt + PLAN_WARPS * E;  // [E]
-    int *before = total + E;          // [E] pairs of the expert in earlier chunks
-    int *first = before + E;          // [E + 1] first block of the expert
+    int *before = total + E;            // [E] pairs of the expert in earlier chunks
+    int *first = before + E;            // [E + 1] first block of the expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunk = blockIdx.x, chunks = gridDim.x;
     for (int i = threadIdx.x; i < (PLAN_WARPS + 2) * E; i += PLAN_THREADS)
@@ -298,27 +482,35 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const PlanRun run(pairs, chunk, chunks, warp);
-    plan_count(ids, run, E, lane, cnt + warp * E);
+    PlanRun run;
+    run.load(ids, pairs, E, chunk, chunks, warp, lane);
+    run.count(cnt + warp * E);
     if (chunks > 1) {
-        // the other chunks' counts: a few chunks per thread and expert, summed in shared memory
-        const int parts = max(1, PLAN_THREADS / E);
-        for (int i = threadIdx.x; i < parts * E; i += PLAN_THREADS) {
-            const int e = i % E, part = i / E;
-            int b = 0, s = 0;
-            for (int c = part; c < chunks; c += parts) {
-                const int h = hist[c * E + e];
-                s += h;
-                b += c < chunk ? h : 0;
+        // all chunks' counts, one warp per expert
+#pragma unroll 4
+        for (int e = warp; e < E; e += PLAN_WARPS) {
+            const int *h = hist + e * PLAN_CHUNKS;
+            int t = 0, b = 0;
+#pragma unroll
+            for (int i = 0; i < PLAN_CHUNKS / 32; ++i) {
+                const int c = i * 32 + lane;
+                const int n = c < chunks ? h[c] : 0;
+                t += n;
+                b += c < chunk ? n : 0;
             }
-            atomicAdd(&total[e], s);
-            atomicAdd(&before[e], b);
+            t = __reduce_add_sync(0xffffffffu, t);
+            b = __reduce_add_sync(0xffffffffu, b);
+            if (lane == 0) {
+                total[e] = t;
+                before[e] = b;
+            }
         }
     }
     __syncthreads();
     // counts of each warp's run -> where the run's first pair of each expert goes
     for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
         int s = before[e];
+#pragma unroll 8
         for (int w = 0; w < PLAN_WARPS; ++w) {
             const int c = cnt[w * E + e];
             cnt[w * E + e] = s;
@@ -351,12 +543,13 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
         for (int e = threadIdx.x; e <= E; e += PLAN_THREADS)
             seg[e] = first[e];
     int *mine = cnt + warp * E;
-    for (int64_t p0 = run.lo; p0 < run.hi; p0 += 32) {
-        const int64_t p = p0 + lane;
-        int id = p < run.hi ? ids[p] : -1;
-        if (id < 0 || id >= E)
-            id = -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, id);
+#pragma unroll
+    for (int i = 0; i < PLAN_REGS; ++i) {
+        const int p = run.lo + 32 * i + lane, id = run.id[i];
+        if (run.lo + 32 * i >= run.hi)
+            break;
+        // (-1 has a bit of its own above those of the experts)
+        const uint32_t same = same_key(uint32_t(id), 33 - __clz(E - 1));
         int at = 0;
         if (id >= 0)
             at = mine[id] + __popc(same & ((1u << lane) - 1u));
@@ -365,19 +558,18 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int64_t pairs, int E,
             mine[id] = at + 1;
         __syncwarp();
         if (p < run.hi) {
-            const int64_t r = id >= 0 ? int64_t(first[id]) * 128 + at : -1;
-            row[p] = int32_t(r);
+            const int r = id >= 0 ? first[id] * 128 + at : -1;
+            row[p] = r;
             if (r >= 0)
-                src[r] = int32_t(p);
+                src[r] = p;
         }
     }
     // rows that no pair takes: the rest of each expert's last block, and all behind the last
     for (int e = chunk * PLAN_WARPS + warp; e < E; e += chunks * PLAN_WARPS)
-        for (int64_t r = int64_t(first[e]) * 128 + total[e] + lane; r < int64_t(first[e + 1]) * 128;
-             r += 32)
+        for (int r = first[e] * 128 + total[e] + lane; r < first[e + 1] * 128; r += 32)
             src[r] = -1;
-    for (int64_t r = int64_t(first[E]) * 128 + int64_t(chunk) * PLAN_THREADS + threadIdx.x; r < rows;
-         r += int64_t(chunks) * PLAN_THREADS)
+    for (int r = first[E] * 128 + chunk * PLAN_THREADS + threadIdx.x; r < rows;
+         r += chunks * PLAN_THREADS)
         src[r] = -1;
 }
 
@@ -475,36 +667,39 @@ int64_t moe_plan_rows(int64_t T, int k, int E)
     return (pairs + 127 * (pairs < E ? pairs : int64_t(E))) / 128 * 128;
 }
 
-size_t moe_plan_workspace(int64_t T, int k, int E)
+size_t moe_plan_workspace(int E)
 {
-    return size_t(plan_chunks(T * k)) * size_t(E) * sizeof(int);
+    return size_t(PLAN_CHUNKS) * size_t(E) * sizeof(int);
 }
 
 cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t *seg,
                             int32_t *row, int32_t *src, void *workspace, cudaStream_t stream)
 {
-    const int64_t pairs = T * k;
+    const int pairs = int(T * k);
     const int chunks = plan_chunks(pairs);
-    const size_t count_smem = size_t(PLAN_WARPS) * E * sizeof(int);
-    const size_t place_smem = count_smem + (3 * size_t(E) + 1) * sizeof(int);
-    if (place_smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(
-            moe_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(moe_plan_count_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    const size_t count_smem = size_t(E) * sizeof(int);
+    const size_t place_smem = ((PLAN_WARPS + 3) * size_t(E) + 1) * sizeof(int);
+    static LaunchCache cache;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (cache.get(dev) == 0) {
+        e = cudaFuncSetAttribute(moe_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 ((PLAN_WARPS + 3) * 1024 + 1) * int(sizeof(int)));
         if (e != cudaSuccess)
             return e;
+        cache.set(dev, 1);
     }
     int *hist = static_cast<int *>(workspace);
     if (chunks > 1) {
-        cudaError_t e = launch(moe_plan_count_kernel, dim3(chunks), PLAN_THREADS, count_smem, stream,
-                               ids, pairs, E, hist);
+        e = launch(moe_plan_count_kernel, dim3(chunks), PLAN_THREADS, count_smem, stream, ids, pairs,
+                   E, hist);
         if (e != cudaSuccess)
             return e;
     }
     return launch(moe_plan_place_kernel, dim3(chunks), PLAN_THREADS, place_smem, stream, ids, pairs,
-                  E, static_cast<const int *>(hist), moe_plan_rows(T, k, E), seg, row, src);
+                  E, static_cast<const int *>(hist), int(moe_plan_rows(T, k, E)), seg, row, src);
 }
 
 } // namespace fp8bw

@@ -25,6 +25,20 @@ __device__ __forceinline__ uint64_t global_timer_ns()
     return t;
 }
 
+// The lanes of a whole warp whose key has the same `bits` low bits: one vote per bit
+// (the match instruction, at about 300 cycles a warp, is several times slower).
+__device__ __forceinline__ uint32_t same_key(uint32_t key, int bits)
+{
+    uint32_t m = 0xffffffffu;
+#pragma unroll 4
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (key >> b) & 1u;
+        const uint32_t v = __ballot_sync(0xffffffffu, set);
+        m &= set ? v : ~v;
+    }
+    return m;
+}
+
 // Register reallocation between warpgroups (whole warpgroup executes it).
 template <uint32_t N>
 __device__ __forceinline__ void regs_dec()

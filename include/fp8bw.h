@@ -246,7 +246,7 @@ int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void 
  *   logits [T][E] FP32 or (bf16 != 0) BF16      weights [T][k] FP32      ids [T][k] int32
  * A logit of -infinity or NaN is never chosen and has probability zero; a row with
  * fewer than k others gets id -1 and weight 0 in the places left.  +infinity counts as
- * the largest finite FP32 value.
+ * the largest finite value of the logits' type.
  */
 int fp8_moe_route(const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
                   float *weights, int32_t *ids, void *stream);

@@ -92,7 +92,7 @@ def weights(gen, e, n, k):
 def route(logits, k, renorm):
     """ids (-1 where nothing is left) and float64 weights, by comparing every pair."""
     v = logits.double()
-    v = torch.where(v > -torch.inf, v.clamp(max=torch.finfo(torch.float32).max), -torch.inf)
+    v = torch.where(v > -torch.inf, v.clamp(max=torch.finfo(logits.dtype).max), -torch.inf)
     e = v.shape[1]
     at = torch.arange(e, device=v.device)
     ahead = (v.unsqueeze(1) > v.unsqueeze(2)) | \

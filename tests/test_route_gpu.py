@@ -62,6 +62,8 @@ def test_route_ties_and_masks(dtype, renorm):
     x[7, 7], x[7, 9] = INF, INF
     x[8, 1:] = torch.finfo(dtype).min
     x[9, 0], x[9, 1:] = -INF, 1.0
+    x[10, 3], x[10, 5] = torch.finfo(dtype).max, INF   # equal: the lower comes first
+    x[11] = -x[11].abs() - 1         # all negative
     w, ids = check_route(x, 6, renorm)
     assert ids[0].tolist() == list(range(6)) and ids[1].tolist() == list(range(6))
     assert ids[2].tolist() == [-1] * 6 and w[2].tolist() == [0.0] * 6

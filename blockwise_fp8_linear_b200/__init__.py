@@ -26,13 +26,14 @@ __all__ = [
     "fp8bw_status_string", "fp8bw_last_device_error", "fp8bw_version",
     "fp8bw_selftest_wait_timeout",
     "linear_fprop", "linear_dgrad", "linear_wgrad",
-    "FEW_TOKENS", "MAX_EXPERTS", "MAX_CHOICES",
+    "MAX_DIM", "FEW_TOKENS", "MAX_EXPERTS", "MAX_CHOICES",
     "fp8_linear_few", "fp8_linear_few_workspace", "fp8_moe_route", "fp8_moe_route_bwd", "fp8_moe_plan_rows", "fp8_moe_plan",
     "fp8_gemm_grouped", "fp8_gemm_grouped_wgrad_acc32", "fp8_moe_few", "fp8_moe_few_workspace",
 ]
 
 FPROP, DGRAD, WGRAD = 0, 1, 2
-FEW_TOKENS, MAX_EXPERTS, MAX_CHOICES = 64, 1024, 32  # the limits of include/fp8bw.h
+# the limits of include/fp8bw.h
+MAX_DIM, FEW_TOKENS, MAX_EXPERTS, MAX_CHOICES = 1 << 20, 64, 1024, 32
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libfp8bw.so")
@@ -113,7 +114,7 @@ def _stream(stream):
     one (asked for as a plain number: making a Stream object costs more than a launch)."""
     import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -131,25 +132,31 @@ def _validate(items):
     raises here (ValueError for shapes and devices, TypeError for kinds)."""
     import torch
     Tensor = torch.Tensor
-    given = [i for i in items if i[0] is not None]
-    for t, _, shp, name in given:
+    for t, _, shp, name in items:
+        if t is None:
+            continue
         if not isinstance(t, Tensor):
             raise TypeError(f"{name} must be a torch tensor")
         if t.shape != shp:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shp)}")
-    for t, dt, _, name in given:
+    devices = []
+    for t, dt, _, name in items:
+        if t is None:
+            continue
         if t.dtype != dt:
             raise TypeError(f"{name} must be {dt}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise TypeError(f"{name} must be a CUDA tensor")
-    first = given[0][0].get_device()
-    for t, _, _, name in given:
-        if t.get_device() != first:
-            raise ValueError(f"{name} is on {t.device}, expected {given[0][0].device} "
-                             "(one device per call)")
-    return given[0][0].device
+        devices.append(d)
+    dev = next(i[0] for i in items if i[0] is not None).device
+    if devices.count(devices[0]) != len(devices):
+        for t, _, _, name in items:
+            if t is not None and t.get_device() != devices[0]:
+                raise ValueError(f"{name} is on {t.device}, expected {dev} (one device per call)")
+    return dev
 
 
 def _alloc(t, shape, dtype, device):
@@ -182,7 +189,7 @@ def _on(device):
     """Context that makes `device` current, so the call's stream and the current device
     match its buffers (the ABI rejects buffers of another device)."""
     import torch
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return _current
     return torch.cuda.device(device)
 
@@ -578,8 +585,8 @@ def fp8_moe_plan_rows(T: int, E: int, k: int) -> int:
     """Rows of the layout by expert that hold any split of T * k pairs over E experts."""
     T, E, k = int(T), int(E), int(k)
     _experts(T, E, k)
-    rows = int(lib().fp8_moe_plan_rows(T, E, k))
-    if rows == 0:
+    rows = (T * k + 127 * min(E, T * k)) // 128 * 128  # as the library has it
+    if rows > MAX_DIM:
         raise ValueError(f"{T} tokens with {k} choices exceed the largest layout")
     return rows
 

@@ -91,13 +91,15 @@ struct FewCfg {
     static constexpr int ACT_WARPS = KIND == FEW_LINEAR ? 4 : KIND == FEW_UP ? 2 : 1;
     static constexpr int ROW_PAIRS = KIND == FEW_UP && BLOCKS == 2 ? 2 : 4;  // quantized at a time
     static constexpr int FIN_WARP0 = ACT_WARP0 + ACT_WARPS;
-    // (up has three: 12 warps leave its promotion warps the registers for their sums)
-    static constexpr int FIN_WARPS = KIND == FEW_UP ? 3 : KIND == FEW_DOWN ? 4 : 0;
+    // Up has three: 12 warps leave its promotion warps the registers for their sums.  Down's
+    // rows wait for memory three times over, about as long as an item's products take.
+    static constexpr int FIN_WARPS = KIND == FEW_UP ? 3 : KIND != FEW_DOWN ? 0 : BLOCKS == 1 ? 8 : 4;
+    static constexpr int RBUF = KIND == FEW_DOWN ? 2 : 1;  // items that may wait to be finished
     static constexpr int THREADS = (FIN_WARP0 + FIN_WARPS) * 32;
     static constexpr int NBUF = 2;
     static constexpr int TMEM_COLS = NBUF * RT * NT;    // 32 .. 128, a power of two
-    // finished sums of one item, [NT][128]; before the first item, scratch of the plan
-    static constexpr int RED_BYTES = EXPERTS ? NT * 128 * 4 : 0;
+    // finished sums of the items, [RBUF][NT][128]; before the first, scratch of the plan
+    static constexpr int RED_BYTES = EXPERTS ? RBUF * NT * 128 * 4 : 0;
     static constexpr int MAX_PAIRS = !EXPERTS ? 0 : NT == 16 ? 16 * 32 : 64 * 32;
     static constexpr int MAX_UNITS = !EXPERTS ? 0 : (NT == 16 ? MAX_PAIRS : 1024) + MAX_PAIRS / NT;
     static constexpr int FIXED = RED_BYTES + (EXPERTS ? 1024 * 10 : 0) + MAX_UNITS * 4 + MAX_PAIRS + 1536;
@@ -109,7 +111,7 @@ struct FewCfg {
     static constexpr int UNIT_OFF = BASE_OFF + (EXPERTS ? 1024 * 2 : 0);  // [MAX_UNITS] unsigned
     static constexpr int TOKEN_OFF = UNIT_OFF + MAX_UNITS * 4;  // [MAX_PAIRS] 8-bit
     static constexpr int BAR_OFF = TOKEN_OFF + MAX_PAIRS;
-    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 2 * NBUF + 2) * 8 + 16;
+    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 2 * NBUF + 2 * RBUF) * 8 + 16;
     static_assert(BAR_OFF % 8 == 0, "barriers are 8-byte words");
     static_assert(RT * NT * 128 * 4 <= STAGES * STAGE_BYTES, "a cluster's parts take the stages");
     static_assert(MAX_PAIRS * 2 <= RED_BYTES, "the plan's scratch");
@@ -320,8 +322,8 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + NBUF;
-    uint64_t *rfull = tempty + NBUF, *rempty = rfull + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rempty + 1);
+    uint64_t *rfull = tempty + NBUF, *rempty = rfull + Cfg::RBUF;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rempty + Cfg::RBUF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     __shared__ int unit_count;
 
@@ -338,8 +340,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 4);
         }
-        mbar_init(rfull, 4);
-        mbar_init(rempty, Cfg::EXPERTS ? Cfg::FIN_WARPS : 1);
+        for (int b = 0; b < Cfg::RBUF; ++b) {
+            mbar_init(&rfull[b], 4);
+            mbar_init(&rempty[b], Cfg::EXPERTS ? Cfg::FIN_WARPS : 1);
+        }
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tmW);
@@ -553,9 +557,12 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                     }
                 continue;
             }
+            const int rb = m % Cfg::RBUF;
+            float *sums = red + rb * NT * 128;
             ok = ok && __all_sync(0xffffffffu,
-                                  mbar_wait_bounded(rempty, (uint32_t(m) & 1u) ^ 1u, abort_flag,
-                                                    &g_few_error, FERR_PROMO, FEW_WAIT_NS));
+                                  mbar_wait_bounded(&rempty[rb], (uint32_t(m / Cfg::RBUF) & 1u) ^ 1u,
+                                                    abort_flag, &g_few_error, FERR_PROMO,
+                                                    FEW_WAIT_NS));
             if (!ok)
                 break;
 #pragma unroll
@@ -565,14 +572,14 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                     if (KIND == FEW_UP)
                         v = make_float2(swiglu(v.x, acc[RT - 1][c / 2].x),
                                         swiglu(v.y, acc[RT - 1][c / 2].y));
-                    red[c * 128 + tid] = v.x;
+                    sums[c * 128 + tid] = v.x;
                 }
                 if (c + 1 < u.rows)
-                    red[(c + 1) * 128 + tid] = v.y;
+                    sums[(c + 1) * 128 + tid] = v.y;
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(rfull);
+                mbar_arrive(&rfull[rb]);
         }
     } else if (warp == 4) {
         // -------------------------------------------------------------- producer
@@ -632,12 +639,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         Walk at;
         for (int n = 0, item = first, m = 0; n < blocks && split == 1; n += nkb, item += step, ++m) {
             enter(at, item);
-            const bool ok = mbar_wait_bounded(rfull, uint32_t(m) & 1u, abort_flag, &g_few_error,
-                                              FERR_FINISH, FEW_WAIT_NS);
+            const int rb = m % Cfg::RBUF;
+            const bool ok = mbar_wait_bounded(&rfull[rb], uint32_t(m / Cfg::RBUF) & 1u, abort_flag,
+                                              &g_few_error, FERR_FINISH, FEW_WAIT_NS);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             for (int r = warp - Cfg::FIN_WARP0; r < at.u.rows; r += Cfg::FIN_WARPS) {
-                const float4 v = *reinterpret_cast<const float4 *>(red + r * 128 + 4 * lane);
+                const float4 v = *reinterpret_cast<const float4 *>(red + (rb * NT + r) * 128 + 4 * lane);
                 if (KIND == FEW_UP)
                     few_store_h(a, at.u.base + r, at.tile, lane, v);
                 else if (KIND == FEW_DOWN)
@@ -647,7 +655,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(rempty);
+                mbar_arrive(&rempty[rb]);
         }
     } else if (Cfg::QUANT) {
         // -------------------------------------------- quantize the tokens' groups
@@ -790,14 +798,23 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 // come from the quantizer's kernel, whose time the next one's start hides.
 constexpr int FEW_QUANT_TOKENS = 16;
 
-// CTAs per item: the reduction is split until the items fill the GPU, with two blocks
-// of 128 left for each CTA at least.
-static int few_split(int64_t items, int64_t KB, int64_t slots)
+// CTAs per item: the split of the reduction that leaves an SM the least time, in blocks of
+// a CTA alone: two CTAs on an SM take 0.8 of their blocks' sum (each hides the other's
+// start and end), a join counts as one block, and each CTA has two blocks at least.  All
+// clusters have to be resident at once (fit[s] of them are): a second round of them costs
+// more than any split gains (61 tokens, 12288 x 2048, 96 items of 16 blocks: 14.5 us
+// split by 2, 19.8 us by 3, of which 93 fit).
+static int few_split(int64_t items, int64_t KB, int64_t sms, const int (&fit)[FEW_MAX_SPLIT + 1])
 {
-    int s = 1;
-    while (s < FEW_MAX_SPLIT && items * s * 2 <= slots && KB >= 4 * s)
-        s *= 2;
-    return s;
+    const auto cost = [&](int s) {
+        const int64_t ctas = (items * s + sms - 1) / sms;
+        return double(ctas * ((KB + s - 1) / s)) * (ctas > 1 ? 0.8 : 1.0) + (s > 1 ? 1.0 : 0.0);
+    };
+    int best = 1;
+    for (int s = 2; s <= FEW_MAX_SPLIT && KB >= 2 * s; ++s)
+        if (items <= fit[s] && cost(s) < cost(best))
+            best = s;
+    return best;
 }
 
 template <class Cfg>
@@ -805,17 +822,40 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
                            cudaStream_t stream, int num_sms)
 {
     auto kern = few_kernel<Cfg>;
-    static LaunchCache cache;
+    static LaunchCache cache[FEW_MAX_SPLIT + 1];  // clusters of each size that fit the GPU
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    if (cache.get(dev) == 0) {
+    if (cache[FEW_MAX_SPLIT].get(dev) == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
         if (e != cudaSuccess)
             return e;
-        cache.set(dev, 1);
+        for (int s = 1; s <= FEW_MAX_SPLIT; ++s) {
+            cudaLaunchConfig_t q = {};
+            cudaLaunchAttribute qa[1];
+            qa[0].id = cudaLaunchAttributeClusterDimension;
+            qa[0].val.clusterDim.x = unsigned(s);
+            qa[0].val.clusterDim.y = 1;
+            qa[0].val.clusterDim.z = 1;
+            q.gridDim = dim3(unsigned(s * num_sms));
+            q.blockDim = dim3(Cfg::THREADS);
+            q.dynamicSmemBytes = Cfg::SMEM;
+            q.attrs = qa;
+            q.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &q);
+            if (e != cudaSuccess)
+                return e;
+            if (n < 1)
+                return cudaErrorInvalidConfiguration;
+            cache[s].set(dev, n);
+        }
     }
+    int fit[FEW_MAX_SPLIT + 1];
+    fit[0] = 0;
+    for (int s = 1; s <= FEW_MAX_SPLIT; ++s)
+        fit[s] = cache[s].get(dev);
     CUtensorMap tw, th;
     if (!codes_map(&tw, w, uint64_t(w_rows), uint64_t(a.K), 128))
         return cudaErrorInvalidValue;
@@ -827,8 +867,8 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
     // those that split theirs have to cover them all.
     const int64_t pairs = int64_t(a.T) * a.k, whole = a.T <= Cfg::NT ? 0 : pairs / Cfg::NT;
     const int64_t units = Cfg::EXPERTS ? (pairs < a.E ? pairs : a.E) + whole : 1;
-    const int64_t items = units * (a.N / 128 / Cfg::RT), slots = int64_t(num_sms) * Cfg::BLOCKS;
-    const int split = few_split(items, a.KB, slots);
+    const int64_t items = units * (a.N / 128 / Cfg::RT), slots = fit[1];
+    const int split = few_split(items, a.KB, num_sms, fit);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     set_pdl(at[0]);

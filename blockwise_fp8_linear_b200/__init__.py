@@ -126,37 +126,50 @@ def _check(status: int, what: str):
 def _validate(items):
     """Check the tensor arguments of one call before anything reaches the C ABI.
     items: (tensor or None, dtype, shape, name); None marks an output to allocate.
-    Shapes are checked first, for every tensor, then dtype, contiguity and that all
-    are CUDA tensors of one device.  A size that disagreed with the M, N, K handed to
-    the C call would let a kernel read or write past an allocation, so every mismatch
-    raises here (ValueError for shapes and devices, TypeError for kinds)."""
+    A size that disagreed with the M, N, K handed to the C call would let a kernel read or
+    write past an allocation, so every mismatch raises here (ValueError for shapes and
+    devices, TypeError for kinds).  Returns the index of their device."""
+    dev = None
+    try:
+        for t, dt, shp, _ in items:
+            if t is None:
+                continue
+            if t.shape != shp or t.dtype is not dt or not t.is_contiguous():
+                break
+            d = t.get_device()
+            if d != dev:
+                if d < 0 or dev is not None:
+                    break
+                dev = d
+        else:
+            return dev
+    except AttributeError:  # not a tensor
+        pass
+    return _refuse(items)
+
+
+def _refuse(items):
+    """Raise for the first fault of _validate's items: shapes come first, for every tensor,
+    then dtype, contiguity and that all are CUDA tensors of one device."""
     import torch
-    Tensor = torch.Tensor
-    for t, _, shp, name in items:
-        if t is None:
-            continue
-        if not isinstance(t, Tensor):
+    given = [i for i in items if i[0] is not None]
+    for t, _, shp, name in given:
+        if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if t.shape != shp:
+        if tuple(t.shape) != tuple(int(d) for d in shp):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shp)}")
-    devices = []
-    for t, dt, _, name in items:
-        if t is None:
-            continue
+    for t, dt, _, name in given:
         if t.dtype != dt:
             raise TypeError(f"{name} must be {dt}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        d = t.get_device()
-        if d < 0:
+        if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        devices.append(d)
-    dev = next(i[0] for i in items if i[0] is not None).device
-    if devices.count(devices[0]) != len(devices):
-        for t, _, _, name in items:
-            if t is not None and t.get_device() != devices[0]:
-                raise ValueError(f"{name} is on {t.device}, expected {dev} (one device per call)")
-    return dev
+    dev = given[0][0].device
+    for t, _, _, name in given:
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev} (one device per call)")
+    return dev.index
 
 
 def _alloc(t, shape, dtype, device):
@@ -168,7 +181,7 @@ def _dims(M, N=None, K=None):
     """Sizes must be positive multiples of 128 (the ABI rejects others; checked here
     so that buffer shapes derived from them are whole)."""
     for d in (M, N, K):
-        if d is not None and (int(d) <= 0 or int(d) % 128):
+        if d is not None and (d <= 0 or d % 128):
             raise ValueError(f"size {d} is not a positive multiple of 128")
 
 
@@ -186,10 +199,10 @@ _current = _Current()
 
 
 def _on(device):
-    """Context that makes `device` current, so the call's stream and the current device
-    match its buffers (the ABI rejects buffers of another device)."""
+    """Context that makes the device of this index current, so the call's stream and the
+    current device match its buffers (the ABI rejects buffers of another device)."""
     import torch
-    if torch._C._cuda_getDevice() == device.index:
+    if torch._C._cuda_getDevice() == device:
         return _current
     return torch.cuda.device(device)
 
@@ -485,17 +498,18 @@ def fp8_linear_few(x, qw, sw, out=None, workspace=None, stream=None):
     M, K = _few_rows(x, "x")
     if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
         raise ValueError("qw must be a 2-D tensor")
-    N = int(qw.shape[0])
-    _dims(N)
+    N = qw.shape[0]
+    _dims(N, K)
     dev = _validate([(x, torch.bfloat16, (M, K), "x"), (qw, torch.uint8, (N, K), "qw"),
                      (sw, torch.float32, (N // 128, K // 128), "sw"),
                      (out, torch.bfloat16, (M, N), "out")])
-    need = lib().fp8_linear_few_workspace(M, K)
+    L = lib()
+    need = L.fp8_linear_few_workspace(M, K)
     with _on(dev):
         out = _alloc(out, (M, N), torch.bfloat16, dev)
         if need:
             workspace = _workspace(workspace, need, dev, stream)
-        _check(lib().fp8_linear_few(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), out.data_ptr(),
+        _check(L.fp8_linear_few(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), out.data_ptr(),
                                     M, N, K, workspace.data_ptr() if need else None,
                                     _stream(stream)), "fp8_linear_few")
     return out
@@ -514,10 +528,9 @@ def _few_rows(x, name):
     import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    M, K = int(x.shape[0]), int(x.shape[1])
+    M, K = x.shape
     if not 1 <= M <= FEW_TOKENS:
         raise ValueError(f"{name} has {M} tokens, expected 1 to {FEW_TOKENS}")
-    _dims(K)
     return M, K
 
 
@@ -539,7 +552,7 @@ def _logits(logits, k):
         raise ValueError("logits must be a 2-D tensor")
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    T, E, k = int(logits.shape[0]), int(logits.shape[1]), int(k)
+    (T, E), k = logits.shape, int(k)
     _experts(T, E, k)
     return T, E, k, logits.dtype == torch.bfloat16
 
@@ -627,9 +640,8 @@ def _workspace(ws, need, dev, stream):
         raise TypeError("workspace must be a uint8 tensor")
     if ws.dim() != 1 or ws.numel() < need:
         raise ValueError(f"workspace has shape {tuple(ws.shape)}, expected ({need},) or longer")
-    _validate([(ws, torch.uint8, ws.shape, "workspace")])
-    if ws.device != dev:
-        raise ValueError(f"workspace is on {ws.device}, expected {dev} (one device per call)")
+    if _validate([(ws, torch.uint8, ws.shape, "workspace")]) != dev:
+        raise ValueError(f"workspace is on {ws.device}, expected cuda:{dev} (one device per call)")
     return ws
 
 
@@ -709,8 +721,8 @@ def fp8_moe_few(x, w1, s1, w2, s2, ids, weights, out=None, workspace=None, strea
             raise ValueError(f"{name} must be a 3-D tensor")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a 2-D tensor")
-    E, I, k = int(w2.shape[0]), int(w2.shape[2]), int(ids.shape[1])
-    _dims(I)
+    (E, _, I), k = w2.shape, ids.shape[1]
+    _dims(H, I)
     _experts(T, E, k)
     dev = _validate([(x, torch.bfloat16, (T, H), "x"),
                      (w1, torch.uint8, (E, 2 * I, H), "w1"),

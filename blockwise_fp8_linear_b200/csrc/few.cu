@@ -71,6 +71,8 @@ struct FewArgs {
     int T, k, E;
     int N, K, KB;            // rows and columns of one expert's weight, K / 128
     int tiles_h;             // H / 128 (up clears the counters)
+    uint32_t tiles_inv;      // 2^32 / tiles of an expert's weight, rounded up (at most 2^32 - 1)
+    int part_lo[FEW_MAX_SPLIT + 1];  // first block of each part of the reduction
 };
 
 template <int KIND_, int NT_>
@@ -329,6 +331,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = int(cluster_ctarank()), split = int(cluster_nctarank());
+    const int first = int(cluster_id_x()), step = int(cluster_count_x());
     int16_t *id = reinterpret_cast<int16_t *>(red);  // scratch of the plan: the pairs' ids
 
     if (tid == 0) {
@@ -400,10 +403,8 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         items *= unit_count;
     }
     // This CTA's items are first, first + step, ...; its part of their reduction is the
-    // blocks lo .. lo + nkb - 1.  Blocks are counted through all its items.
-    const int first = int(blockIdx.x) / split, step = int(gridDim.x) / split;
-    const int lo = a.KB * rank / split, nkb = a.KB * (rank + 1) / split - lo;
-    const int blocks = first < items ? ((items - 1 - first) / step + 1) * nkb : 0;
+    // blocks lo .. lo + nkb - 1.  (No divisions here: nothing is loaded before this is done.)
+    const int lo = a.part_lo[rank], nkb = a.part_lo[rank + 1] - lo;
     // A place in that walk: an item, and the block within its part.
     struct Walk {
         int item, i, tile;
@@ -414,9 +415,17 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         w.u = {0, 0, a.T};
         w.tile = item;
         if (Cfg::EXPERTS && item < items) {
-            const int unit = item / tiles;
+            // item / tiles by its inverse, which is off by one at most
+            int unit = int(__umulhi(uint32_t(item), a.tiles_inv)), tile = item - unit * tiles;
+            if (tile < 0) {
+                --unit;
+                tile += tiles;
+            } else if (tile >= tiles) {
+                ++unit;
+                tile -= tiles;
+            }
             w.u = FewUnit::of(plan.units[unit]);
-            w.tile = item - unit * tiles;
+            w.tile = tile;
         }
     };
     const auto start = [&](int i) {
@@ -446,12 +455,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             tma_load_2d_hint(dst + 128 * 128, &tmW, &full[s], (lo + w.i) * 128, row + a.N / 2, once);
     };
     // weights do not wait for the order of the rows, nor for the kernel before
-    const int early = min(STAGES, blocks);
-    if (warp == 4 && lane == 0) {
-        Walk w = start(0);
-        for (int n = 0; n < early; ++n, advance(w, 1))
-            load_weights(w, n);
-    }
+    int early = 0;
+    if (warp == 4 && lane == 0)
+        for (Walk w = start(0); early < STAGES && w.item < items; ++early, advance(w, 1))
+            load_weights(w, early);
     if (Cfg::EXPERTS) {
         for (int i = tid; i < a.T * a.k; i += Cfg::THREADS)
             if (id[i] >= 0)
@@ -470,14 +477,14 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             for (int r = 0; r < RT; ++r)
                 sw[r] = a.sw + (size_t(w.u.expert) * n_tiles + w.tile + r * tiles) * a.KB + lo;
         };
-        if (blocks > 0) {
+        if (first < items) {
             scales_of(at);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
                 next[r] = __ldg(sw[r]);
         }
         bool ok = true;
-        for (int n = 0, m = 0; n < blocks && ok; at = to, ++m) {
+        for (int n = 0, m = 0; at.item < items && ok; at = to, ++m) {
             const FewUnit u = at.u;
             const int cols = columns(u.rows);
             enter(to, at.item + step);
@@ -491,12 +498,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
                 const int s = n % STAGES, b = n % NBUF;
                 float2 cur[RT];
                 const bool more = i + 1 < nkb;
-                if (!more && n + 1 < blocks)
+                const bool next_item = !more && to.item < items;
+                if (next_item)
                     scales_of(to);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     cur[r] = make_float2(next[r], next[r]);
-                    if (n + 1 < blocks)
+                    if (more || next_item)
                         next[r] = __ldg(sw[r] + (more ? i + 1 : 0));
                 }
                 // the stage's full barrier cannot run ahead: it waits for this warp below
@@ -583,13 +591,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         }
     } else if (warp == 4) {
         // -------------------------------------------------------------- producer
-        if (lane == 0 && blocks > 0) {
+        if (lane == 0 && first < items) {
             if (!Cfg::QUANT) {
                 pdl_wait();
                 pdl_launch_dependents();
             }
             Walk w = start(0);
-            for (int n = 0; n < blocks; ++n, advance(w, 1)) {
+            for (int n = 0; w.item < items; ++n, advance(w, 1)) {
                 const int s = n % STAGES;
                 if (n >= early) {
                     if (!mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
@@ -607,12 +615,9 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         if (lane == 0) {
             static_assert(NBUF == 2, "one MMA warp per buffer");
             const int b = warp - 5;
-            Walk w = {};
-            if (b < blocks) {
-                w = start(0);
-                advance(w, b);
-            }
-            for (int n = b; n < blocks; n += NBUF, advance(w, NBUF)) {
+            Walk w = start(0);
+            advance(w, b);
+            for (int n = b; w.item < items; n += NBUF, advance(w, NBUF)) {
                 const int s = n % STAGES;
                 const uint32_t idesc = make_idesc_e4m3(128, columns(w.u.rows), 0);
                 if (!mbar_spin_bounded(&full[s], uint32_t(n / STAGES) & 1u, abort_flag, &g_few_error,
@@ -637,7 +642,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     } else if (Cfg::EXPERTS && warp >= Cfg::FIN_WARP0) {
         // --------------------------------------------------------- finish the rows
         Walk at;
-        for (int n = 0, item = first, m = 0; n < blocks && split == 1; n += nkb, item += step, ++m) {
+        for (int item = first, m = 0; item < items && split == 1; item += step, ++m) {
             enter(at, item);
             const int rb = m % Cfg::RBUF;
             const bool ok = mbar_wait_bounded(&rfull[rb], uint32_t(m / Cfg::RBUF) & 1u, abort_flag,
@@ -675,13 +680,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
             }
         };
         uint4 v[P], ahead[P];
-        Walk w = {}, next;
-        if (blocks > 0) {
-            w = start(0);
-            advance(w, warp - Cfg::ACT_WARP0);
-            fetch(w, 0, v);
-        }
-        for (int n = warp - Cfg::ACT_WARP0; n < blocks; n += Cfg::ACT_WARPS, w = next) {
+        Walk w = start(0), next;
+        advance(w, warp - Cfg::ACT_WARP0);
+        fetch(w, 0, v);
+        for (int n = warp - Cfg::ACT_WARP0; w.item < items; n += Cfg::ACT_WARPS, w = next) {
             const int s = n % STAGES, rows = w.u.rows;
             next = w;
             advance(next, Cfg::ACT_WARPS);
@@ -711,10 +713,8 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
     } else {
         // --------------------------------------------------- scales of the codes
         pdl_wait();
-        Walk w = {};
-        if (blocks > 0)
-            w = start(0);
-        for (int n = 0; n < blocks; ++n, advance(w, 1)) {
+        Walk w = start(0);
+        for (int n = 0; w.item < items; ++n, advance(w, 1)) {
             const int s = n % STAGES;
             const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
                                               &g_few_error, FERR_ACT, FEW_WAIT_NS);
@@ -818,7 +818,7 @@ static int few_split(int64_t items, int64_t KB, int64_t sms, const int (&fit)[FE
 }
 
 template <class Cfg>
-static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *codes, const FewArgs &a,
+static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *codes, FewArgs a,
                            cudaStream_t stream, int num_sms)
 {
     auto kern = few_kernel<Cfg>;
@@ -869,6 +869,10 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
     const int64_t units = Cfg::EXPERTS ? (pairs < a.E ? pairs : a.E) + whole : 1;
     const int64_t items = units * (a.N / 128 / Cfg::RT), slots = fit[1];
     const int split = few_split(items, a.KB, num_sms, fit);
+    for (int s = 0; s <= split; ++s)
+        a.part_lo[s] = int(int64_t(a.KB) * s / split);
+    const uint64_t tiles = uint64_t(a.N / 128 / Cfg::RT);
+    a.tiles_inv = tiles == 1 ? 0xFFFFFFFFu : uint32_t(((uint64_t(1) << 32) + tiles - 1) / tiles);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     set_pdl(at[0]);

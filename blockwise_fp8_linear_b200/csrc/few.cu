@@ -803,7 +803,7 @@ constexpr int FEW_QUANT_TOKENS = 16;
 // start and end), a join counts as one block, and each CTA has two blocks at least.  All
 // clusters have to be resident at once (fit[s] of them are): a second round of them costs
 // more than any split gains (61 tokens, 12288 x 2048, 96 items of 16 blocks: 14.5 us
-// split by 2, 19.8 us by 3, of which 93 fit).
+// split by 2, 19.8 us by 3, of which fewer fit).
 static int few_split(int64_t items, int64_t KB, int64_t sms, const int (&fit)[FEW_MAX_SPLIT + 1])
 {
     const auto cost = [&](int s) {
@@ -849,7 +849,10 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
                 return e;
             if (n < 1)
                 return cudaErrorInvalidConfiguration;
-            cache[s].set(dev, n);
+            // The query counts one CTA per SM for a kernel that holds tensor memory.  Two whose
+            // registers, shared and tensor memory fit do share an SM (seen by their SM numbers
+            // and times: 192 CTAs on 148 SMs, 44 of them with two at once).
+            cache[s].set(dev, n * Cfg::BLOCKS);
         }
     }
     int fit[FEW_MAX_SPLIT + 1];

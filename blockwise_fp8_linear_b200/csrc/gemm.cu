@@ -488,14 +488,33 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         for (int i = 0; i < COLS / 2; ++i)
             acc[i] = make_float2(0.f, 0.f);
 
-        int buf = 0, kb = 0, t = unit, j = 0;
+        const int my_tiles = (num_tiles - unit + units - 1) / units;
+        const int total_iters = my_tiles > 0 ? my_tiles * KB : 0;
+
+        int buf = 0, kb = 0, t = unit;
         uint32_t tphase = 0;
         Tile o = {};
-        if (t < num_tiles)
+        // Grouped wgrad: the tiles of an expert without tokens have no blocks; they are
+        // zeros (nothing to add with OUT32).
+        const auto skip_empty = [&]() {
+            if constexpr (Cfg::GROUPED && MODE == 2) {
+                while (t < num_tiles && o.kbs == 0) {
+                    if (!Cfg::OUT32) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            D + size_t(o.drow + row_local) * size_t(N) + size_t(o.tn * BN + col0));
+                        for (int c = 0; c < COLS / 8; ++c)
+                            dst[c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    t += units;
+                    if (t < num_tiles)
+                        o = locate(t);
+                }
+            }
+        };
+        if (!Cfg::GROUPED || t < num_tiles)
             o = locate(t);
-        while (t < num_tiles) {
-            // (an expert without tokens has no blocks: its wgrad tile is stored as zeros)
-            if (!(Cfg::GROUPED && MODE == 2) || o.kbs > 0) {
+        skip_empty();
+        for (int j = 0; Cfg::GROUPED ? t < num_tiles : j < total_iters; ++j) {
             const int r = j % Cfg::SRING;
             const bool sready = mbar_wait_bounded(&sfull[r], uint32_t(j / Cfg::SRING) & 1u,
                                                   abort_flag, &g_device_error, ERR_SCALES,
@@ -625,14 +644,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sempty[r]);  // this warp is done with the slot's scales
-            ++kb;
-            ++j;
-            if (++buf == Cfg::NBUF) {
-                buf = 0;
-                tphase ^= 1u;
-            }
-            }
-            if (kb == o.kbs) {
+            if (++kb == (Cfg::GROUPED && MODE == 2 ? o.kbs : KB)) {
                 const int tn = o.tn;
                 if constexpr (Cfg::OUT32 && Cfg::TMA_STORE) {
                     // FP32 tile -> swizzled staging (32 rows x 64 columns per pass, two
@@ -642,8 +654,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const int r0 = o.drow + quarter * 32;
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
-                        if (Cfg::GROUPED && o.kbs == 0)
-                            break;  // nothing to add
                         if (lane == 0)
                             bulk_wait_read0();
                         __syncwarp();
@@ -672,8 +682,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     float *dst = D32 + size_t(o.drow + row_local) * size_t(N) + size_t(tn * BN + col0);
 #pragma unroll
                     for (int c = 0; c < COLS / 4; ++c)
-                        if (!Cfg::GROUPED || o.kbs > 0)
-                            atomicAdd(reinterpret_cast<float4 *>(dst + 4 * c),
+                        atomicAdd(reinterpret_cast<float4 *>(dst + 4 * c),
                                   make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
                                               acc[2 * c + 1].y));
                 } else if (Cfg::GROUPED && !o.live) {
@@ -753,6 +762,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 t += units;
                 if (t < num_tiles)
                     o = locate(t);
+                skip_empty();
+            }
+            if (++buf == Cfg::NBUF) {
+                buf = 0;
+                tphase ^= 1u;
             }
         }
         if (Cfg::TMA_STORE && lane == 0)

@@ -101,6 +101,32 @@ def lib():
     return _lib
 
 
+# The compiled calls (csrc/calls.cpp): each takes the arguments of the function that it
+# stands in for and makes the plain call, or returns NotImplemented.
+_calls = None
+
+
+def _open_calls():
+    """Load _calls.so and hand it the library's entry points."""
+    global _calls
+    import torch  # noqa: F401  (its libraries have to be there)
+    L = lib()
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m blockwise_fp8_linear_b200.build`")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("_calls", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.open(Fp8bwError, *[C.cast(getattr(L, n), C.c_void_p).value for n in (
+        "fp8_linear_few_workspace", "fp8_linear_few", "fp8_moe_route", "fp8_moe_route_bwd",
+        "fp8_moe_plan_rows", "fp8_moe_plan_workspace", "fp8_moe_plan", "fp8_gemm_grouped",
+        "fp8_gemm_grouped_wgrad_acc32", "fp8_moe_few_workspace", "fp8_moe_few")])
+    _calls = m
+    return m
+
+
 def fp8bw_status_string(status: int) -> str:
     return lib().fp8bw_status_string(int(status)).decode()
 
@@ -494,6 +520,9 @@ def fp8_linear_few(x, qw, sw, out=None, workspace=None, stream=None):
     quantized by fp8_quant_weight; X is quantized inside the call as by fp8_quant_act.
     workspace: uint8, fp8_linear_few_workspace(M, K) bytes or more, one for each call (or
     captured graph) that may run at the same time."""
+    r = (_calls or _open_calls()).linear_few(x, qw, sw, out, workspace, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     M, K = _few_rows(x, "x")
     if not isinstance(qw, torch.Tensor) or qw.dim() != 2:
@@ -561,6 +590,9 @@ def fp8_moe_route(logits, k: int, renorm: bool = True, weights=None, ids=None, s
     """logits[T][E] (float32 or bf16) -> (weights[T][k] float32, ids[T][k] int32): the k
     largest, ties to the lowest expert, with softmax weights over the chosen experts
     (renorm) or over all.  -inf and NaN are never chosen (id -1, weight 0)."""
+    r = (_calls or _open_calls()).moe_route(logits, k, renorm, weights, ids, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     T, E, k, bf16 = _logits(logits, k)
     dev = _validate([(logits, logits.dtype, (T, E), "logits"),
@@ -578,6 +610,9 @@ def fp8_moe_route_bwd(dweights, weights, ids, logits, renorm: bool = True, dlogi
                       stream=None):
     """Gradient of the logits (of their type) from that of the weights; weights, ids,
     logits and renorm as in the forward call."""
+    r = (_calls or _open_calls()).moe_route_bwd(dweights, weights, ids, logits, renorm, dlogits, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a 2-D tensor")
@@ -608,6 +643,9 @@ def fp8_moe_plan(ids, E: int, seg=None, row=None, src=None, workspace=None, stre
     """ids[T][k] int32 -> (seg[E + 1], row[T][k], src[rows]) int32: expert e owns the blocks of
     128 rows seg[e] .. seg[e + 1] - 1; row is each pair's row (-1: left out), src each row's
     pair t * k + j (-1: none).  workspace: uint8, at least what the header asks for."""
+    r = (_calls or _open_calls()).moe_plan(ids, E, seg, row, src, workspace, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a 2-D tensor")
@@ -668,6 +706,9 @@ def fp8_gemm_grouped(mode: int, a, sa, b, sb, seg, M: int, N: int, K: int, out=N
     seg[e] .. seg[e + 1] - 1 (see fp8_moe_plan and include/fp8bw.h).  FPROP and DGRAD give
     [M][N] and leave the rows of blocks that no expert owns as they were; WGRAD gives
     [E][M][N]."""
+    r = (_calls or _open_calls()).gemm_grouped(mode, a, sa, b, sb, seg, M, N, K, out, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     M, N, K = int(M), int(N), int(K)
     E, sh_a, sh_sa, sh_b, sh_sb, sh_d = _grouped_shapes(mode, M, N, K, seg)
@@ -684,6 +725,9 @@ def fp8_gemm_grouped(mode: int, a, sa, b, sb, seg, M: int, N: int, K: int, out=N
 
 def fp8_gemm_grouped_wgrad_acc32(a, sa, b, sb, seg, M: int, N: int, K: int, dw32, stream=None):
     """dw32[E][M][N] (float32, caller-owned) += the grouped WGRAD, kept in FP32."""
+    r = (_calls or _open_calls()).gemm_grouped_wgrad_acc32(a, sa, b, sb, seg, M, N, K, dw32, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     M, N, K = int(M), int(N), int(K)
     E, sh_a, sh_sa, sh_b, sh_sb, sh_d = _grouped_shapes(WGRAD, M, N, K, seg)
@@ -714,6 +758,9 @@ def fp8_moe_few(x, w1, s1, w2, s2, ids, weights, out=None, workspace=None, strea
     s2[E][H/128][I/128] as fp8_quant_weight gives them; ids, weights[T][k] as from
     fp8_moe_route.  workspace: uint8, fp8_moe_few_workspace(T, k, H, I) bytes or more, one
     for each call (or captured graph) that may run at the same time."""
+    r = (_calls or _open_calls()).moe_few(x, w1, s1, w2, s2, ids, weights, out, workspace, stream)
+    if r is not NotImplemented:
+        return r
     import torch
     T, H = _few_rows(x, "x")
     for t, name in ((w1, "w1"), (w2, "w2")):

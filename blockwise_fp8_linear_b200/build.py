@@ -1,4 +1,5 @@
-"""Build ``libfp8bw.so`` (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build ``libfp8bw.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and ``_calls.so``
+(the binding's compiled calls, against the installed torch) with g++.
 
 Usage: ``python -m blockwise_fp8_linear_b200.build [--force] [--verbose]``.
 Rebuilds only when a source or header is newer than the library.  IEEE division and
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8bw.so")
+CALLS = os.path.join(HERE, "_calls.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -40,7 +42,32 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
+def build_calls(force: bool = False) -> str:
+    """The compiled calls; rebuilt when their source, the header or torch is newer."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    src = os.path.join(CSRC, "calls.cpp")
+    deps = [src, os.path.join(INCLUDE, "fp8bw.h"), torch.__file__, __file__]
+    if not force and os.path.exists(CALLS) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return CALLS
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(),
+           os.path.join(cuda, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                    "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                    *[f"-I{i}" for i in inc], src, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch",
+                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_calls(force)
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(p) <= t for p in _deps()):

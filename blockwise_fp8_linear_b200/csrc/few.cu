@@ -793,10 +793,15 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------- host side
 
-// The linear quantizes its tokens itself up to this many.  Beyond, every tile's CTAs
-// would quantize them anew for longer than their weights take to arrive, and the codes
-// come from the quantizer's kernel, whose time the next one's start hides.
-constexpr int FEW_QUANT_TOKENS = 16;
+// Whether the linear quantizes its tokens itself.  Every tile's CTAs quantize them anew;
+// beyond some tokens that takes longer than their weights take to arrive, and the codes
+// come from the quantizer's kernel instead, a launch more, whose time the next one's start
+// hides.  Measured (itself / codes): 8 tokens 5.0 / 6.1 us at 2048 x 2048 and 28.9 / 29.9 at
+// 12288 x 12288; 16 tokens 6.1 / 6.5, 10.2 / 9.3 (12288 x 2048) and 39.2 / 30.5; 32 tokens
+// 9.6 / 7.2 at 2048 x 2048.
+constexpr int FEW_QUANT_TOKENS = 8;        // at any size
+constexpr int FEW_QUANT_TOKENS_SMALL = 16; // of a weight below this many elements
+constexpr int64_t FEW_QUANT_SMALL = int64_t(1) << 25;
 
 // CTAs per item: the split of the reduction that leaves an SM the least time, in blocks of
 // a CTA alone: two CTAs on an SM take 0.8 of their blocks' sum (each hides the other's
@@ -896,7 +901,7 @@ static cudaError_t run_few(const uint8_t *w, int64_t w_rows, const uint8_t *code
 
 size_t linear_few_workspace(int T, int64_t K)
 {
-    // codes, then scales
+    // codes, then scales (a small weight does without)
     return T <= FEW_QUANT_TOKENS ? 0 : size_t(T) * K + size_t(T) * (K / 128) * 4;
 }
 
@@ -913,7 +918,7 @@ cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const flo
     a.N = int(N);
     a.K = int(K);
     a.KB = int(K / 128);
-    if (T <= FEW_QUANT_TOKENS)
+    if (T <= FEW_QUANT_TOKENS || (T <= FEW_QUANT_TOKENS_SMALL && N * K < FEW_QUANT_SMALL))
         return run_few<FewCfg<FEW_LINEAR, 16>>(qw, N, nullptr, a, stream, num_sms);
     uint8_t *q = static_cast<uint8_t *>(workspace);
     float *s = reinterpret_cast<float *>(q + size_t(T) * K);
@@ -922,6 +927,8 @@ cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const flo
     const cudaError_t e = launch_quant_act(x, T, K, q, s, stream, num_sms);
     if (e != cudaSuccess)
         return e;
+    if (T <= 16)
+        return run_few<FewCfg<FEW_CODES, 16>>(qw, N, q, a, stream, num_sms);
     return T <= 32 ? run_few<FewCfg<FEW_CODES, 32>>(qw, N, q, a, stream, num_sms)
                    : run_few<FewCfg<FEW_CODES, 64>>(qw, N, q, a, stream, num_sms);
 }

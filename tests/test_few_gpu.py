@@ -32,7 +32,8 @@ def test_linear_tokens(m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 2048, 2048), (3, 128, 12288), (64, 128, 6144), (5, 4096, 256),
-                                   (20, 12288, 128), (40, 6144, 2048), (1, 128, 128 * 129), (64, 20480, 384)])
+                                   (20, 12288, 128), (40, 6144, 2048), (1, 128, 128 * 129), (64, 20480, 384),
+                                   (8, 8192, 4096), (9, 8192, 4096), (16, 8192, 4096), (13, 12288, 12288)])
 def test_linear_shapes(m, n, k):
     g = gen(n + k)
     qw, sw = weights(g, 1, n, k)
@@ -175,3 +176,46 @@ def test_layer_workspace():
         fb.fp8_moe_few(*a, workspace=ws[:need - 16])
     with pytest.raises(TypeError):
         fb.fp8_moe_few(*a, workspace=ws.view(torch.int32))
+
+
+def test_misaligned_and_strided_arguments():
+    g = gen(15)
+    qw, sw = weights(g, 1, 256, 256)
+    buf = acts(g, 9, 256).view(-1)
+    with pytest.raises(fb.Fp8bwError) as e:
+        fb.fp8_linear_few(buf[4:4 + 8 * 256].view(8, 256), qw[0], sw[0])   # 8 bytes off
+    assert e.value.status == 2
+    wide = acts(g, 8, 512)
+    with pytest.raises(ValueError):
+        fb.fp8_linear_few(wide[:, :256], qw[0], sw[0])                     # rows with a gap
+    assert torch.equal(fb.fp8_linear_few(wide[:, :256].contiguous(), qw[0], sw[0]),
+                       fb.fp8_linear_few(wide[:, :256].contiguous(), qw[0], sw[0],
+                                         stream=torch.cuda.current_stream()))
+    # a Parameter is a tensor like any other
+    x = torch.nn.Parameter(wide[:, :256].contiguous())
+    assert torch.equal(fb.fp8_linear_few(x, qw[0], sw[0]),
+                       fb.fp8_linear_few(x.detach(), qw[0], sw[0]))
+
+
+def test_compiled_calls_and_python_agree():
+    """The compiled form of each call and the Python one (taken for an explicit stream)."""
+    a = make_layer(gen(16), 21, 6, 3, 256, 256)
+    st = torch.cuda.current_stream()
+    qw, sw = a[1][0], a[2][0]
+    assert torch.equal(fb.fp8_linear_few(a[0], qw, sw), fb.fp8_linear_few(a[0], qw, sw, stream=st))
+    assert torch.equal(fb.fp8_moe_few(*a), fb.fp8_moe_few(*a, stream=st))
+    lg = torch.randn(21, 6, generator=gen(1), device="cuda")
+    one, two = fb.fp8_moe_route(lg, 2, False), fb.fp8_moe_route(lg, 2, False, stream=st)
+    assert all(torch.equal(u, v) for u, v in zip(one, two))
+    dw = torch.randn(21, 2, generator=gen(2), device="cuda")
+    assert torch.equal(fb.fp8_moe_route_bwd(dw, *one, lg, False), fb.fp8_moe_route_bwd(dw, *one, lg, False, stream=st))
+    p1, p2 = fb.fp8_moe_plan(one[1], 6), fb.fp8_moe_plan(one[1], 6, stream=st)
+    assert all(torch.equal(u, v) for u, v in zip(p1, p2))
+    rows = p1[2].numel()
+    q, s = fb.fp8_quant_act(acts(gen(3), rows, 256))
+    g1 = fb.fp8_gemm_grouped(fb.FPROP, q, s, a[1], a[2], p1[0], rows, 512, 256, out=torch.zeros(rows, 512, dtype=torch.bfloat16, device="cuda"))
+    g2 = fb.fp8_gemm_grouped(fb.FPROP, q, s, a[1], a[2], p1[0], rows, 512, 256, stream=st, out=torch.zeros_like(g1))
+    assert torch.equal(g1, g2)
+    # numpy integers and the like are taken by the Python form
+    import numpy as np
+    assert torch.equal(fb.fp8_moe_route(lg, np.int64(2), False)[1], one[1])

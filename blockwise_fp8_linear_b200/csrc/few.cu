@@ -150,6 +150,30 @@ struct FewPlan {
     }
     __device__ __forceinline__ int row(int e, int t) const { return base[e] + before(e, t); }
 
+    // The same from the ids of at most 32 pairs, a lane each (-1: none), whatever E: one
+    // step in the place of one per 32 experts.  The experts stand in the order in which the
+    // pairs name them, which only this kernel and the next have to agree on.
+    template <int NT> __device__ __forceinline__ int make_units_of(int id, int E, int lane) const
+    {
+        const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+        const uint32_t same = same_key(uint32_t(id), 32 - __clz(E - 1)) & live;
+        const bool first = id >= 0 && __ffs(same) - 1 == lane;
+        const int c = first ? __popc(mask[2 * id]) + __popc(mask[2 * id + 1]) : 0;
+        const int u = (c + NT - 1) / NT;
+        int sum = u << 16 | c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= o ? up : 0;
+        }
+        const int row0 = (sum & 0xFFFF) - c, unit = (sum >> 16) - u;
+        if (first)
+            base[id] = uint16_t(row0);
+        for (int i = 0; i < u; ++i)
+            units[unit + i] = FewUnit::pack(id, row0 + i * NT, min(NT, c - i * NT));
+        return __shfl_sync(0xffffffffu, sum, 31) >> 16;
+    }
+
     // Masks -> first rows and units of at most NT rows.  One warp; returns how many units.
     template <int NT> __device__ __forceinline__ int make_units(int E, int lane) const
     {
@@ -395,7 +419,10 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         }
         __syncthreads();
         if (warp == 4) {
-            const int n = plan.make_units<NT>(a.E, lane);
+            const int pairs = a.T * a.k;
+            const int n = pairs <= 32
+                              ? plan.make_units_of<NT>(lane < pairs ? int(id[lane]) : -1, a.E, lane)
+                              : plan.make_units<NT>(a.E, lane);
             if (lane == 0)
                 unit_count = n;
         }

@@ -831,16 +831,19 @@ constexpr int FEW_QUANT_TOKENS_SMALL = 16; // of a weight below this many elemen
 constexpr int64_t FEW_QUANT_SMALL = int64_t(1) << 25;
 
 // CTAs per item: the split of the reduction that leaves an SM the least time, in blocks of
-// a CTA alone: two CTAs on an SM take 0.8 of their blocks' sum (each hides the other's
-// start and end), a join counts as one block, and each CTA has two blocks at least.  All
-// clusters have to be resident at once (fit[s] of them are): a second round of them costs
-// more than any split gains (61 tokens, 12288 x 2048, 96 items of 16 blocks: 14.5 us
-// split by 2, 19.8 us by 3, of which fewer fit).
+// a CTA alone: two CTAs on an SM take 0.7 of their blocks' sum (each hides the other's
+// start and end), a join counts as two blocks, and each CTA has two blocks at least.
+// (Measured by split, 1 .. 8: up of one token and 8 experts, 48 items of 16 blocks: 29.9 /
+// 24.3 / 22.9 / 22.0 / 22.4 / 28.7 us for the layer; 7 tokens, 2048 x 6144, 16 items of 48
+// blocks, by 2 .. 6 and 8: 11.5 / 9.0 / 7.9 / 7.3 / 6.8 / 6.6 us.)  All clusters have to be
+// resident at once (fit[s] of them are): a second round of them costs more than any
+// split gains (61 tokens, 12288 x 2048, 96 items of 16 blocks: 14.5 us split by 2, 19.8 us
+// by 3, of which fewer fit).
 static int few_split(int64_t items, int64_t KB, int64_t sms, const int (&fit)[FEW_MAX_SPLIT + 1])
 {
     const auto cost = [&](int s) {
         const int64_t ctas = (items * s + sms - 1) / sms;
-        return double(ctas * ((KB + s - 1) / s)) * (ctas > 1 ? 0.8 : 1.0) + (s > 1 ? 1.0 : 0.0);
+        return double(ctas * ((KB + s - 1) / s)) * (ctas > 1 ? 0.7 : 1.0) + (s > 1 ? 2.0 : 0.0);
     };
     int best = 1;
     for (int s = 2; s <= FEW_MAX_SPLIT && KB >= 2 * s; ++s)

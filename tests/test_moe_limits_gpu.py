@@ -1,0 +1,169 @@
+"""Few-token and mixture-of-experts calls at the ends of their ranges: the largest sizes of
+one dimension, the most choices, offsets past 32 bits, two calls at once."""
+import pytest
+import torch
+
+import blockwise_fp8_linear_b200 as fb
+from _moe import acts, blocks64, check, check_bf16, dequant_rows, layer, rows64, sum_bound, weights
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 128, 1 << 20), (33, 128, 1 << 20), (64, 1 << 20, 128), (2, 1 << 20, 256)])
+def test_linear_longest_sides(m, n, k):
+    g = gen(m)
+    x = acts(g, m, k)
+    qw, sw = weights(g, 1, n, k)
+    y = fb.fp8_linear_few(x, qw[0], sw[0])
+    a = dequant_rows(x)
+    step = 1 << 14 if n > 128 else 128
+    for lo in range(0, n, step):
+        cut = slice(lo, lo + step)
+        w = blocks64(qw[0][cut], sw[0][lo // 128:(lo + step) // 128])
+        check_bf16(y[:, cut], a @ w.t(), a.abs() @ w.abs().t(), k, f"columns from {lo}")
+
+
+def make(g, t, e, k, h, i):
+    x = acts(g, t, h)
+    # the gate and the up rows quantized apart: one call takes no more than fb.MAX_DIM rows
+    halves = [weights(g, e, i, h) for _ in range(2)]
+    w1, s1 = (torch.cat(t, 1) for t in zip(*halves))
+    w2, s2 = weights(g, e, h, i)
+    wt, ids = fb.fp8_moe_route(torch.randn(t, e, generator=g, device="cuda"), k)
+    return [x, w1, s1, w2, s2, ids, wt]
+
+
+@pytest.mark.parametrize("t,e,k,h,i", [
+    (64, 32, 32, 128, 128),      # every token chooses every expert: two units of rows each
+    (16, 1024, 32, 128, 128),    # the most experts that 16 tokens can hit
+    (64, 1024, 32, 128, 128),
+    (2, 1, 1, 1 << 20, 128), (33, 2, 2, 1 << 19, 128), (2, 1, 1, 128, 1 << 19), (2, 1, 1, 128, 1 << 20), (20, 2, 1, 128, 1 << 18)])
+def test_layer_ends_of_the_ranges(t, e, k, h, i):
+    a = make(gen(t + e), t, e, k, h, i)
+    y = fb.fp8_moe_few(*a)
+    torch.cuda.synchronize()
+    assert fb.fp8bw_last_device_error() == 0
+    ref, slack = layer(*a)
+    check(y, ref, slack, "layer")
+
+
+def last_expert(g, e, n, k):
+    """E experts' weights of more than 4 GB, all zero but the last one's."""
+    w, s = torch.zeros(e, n, k, dtype=torch.uint8, device="cuda"), torch.zeros(e, n // 128, k // 128, device="cuda")
+    q, sc = weights(g, 1, n, k)
+    w[-1], s[-1] = q[0], sc[0]
+    return w, s
+
+
+def test_layer_weights_past_4_gb():
+    g = gen(2)
+    t, e, h, i = 5, 1024, 2048, 1152
+    w1, s1 = last_expert(g, e, 2 * i, h)
+    w2, s2 = last_expert(g, e, h, i)
+    assert w1.numel() > 1 << 32
+    x = acts(g, t, h)
+    ids = torch.tensor([[e - 1, 0]] * t, dtype=torch.int32, device="cuda")
+    wt = torch.rand(t, 2, generator=g, device="cuda")
+    y = fb.fp8_moe_few(x, w1, s1, w2, s2, ids, wt)
+    # expert 0 is all zero: the last one alone counts
+    ref, slack = layer(x, w1[-1:], s1[-1:], w2[-1:], s2[-1:], torch.zeros_like(ids[:, :1]), wt[:, :1])
+    check(y, ref, slack, "layer")
+
+
+@pytest.mark.parametrize("mode", [fb.FPROP, fb.DGRAD])
+def test_grouped_weights_past_4_gb(mode):
+    g = gen(3)
+    e, n, k, blocks = 600, 2048, 4096, 3
+    b, sb = last_expert(g, e, n, k) if mode == fb.FPROP else last_expert(g, e, k, n)
+    assert b.numel() > 1 << 32
+    a, sa = fb.fp8_quant_act(acts(g, 128 * blocks, k))
+    seg = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    seg[1:] = 1
+    seg[-1] = blocks             # one block for expert 0, the rest for the last
+    d = fb.fp8_gemm_grouped(mode, a, sa, b, sb, seg, 128 * blocks, n, k)
+    assert (d[:128] == 0).all()
+    a64 = rows64(a, sa)[128:]
+    w = blocks64(b[-1], sb[-1])
+    w = w.t() if mode == fb.FPROP else w
+    check_bf16(d[128:], a64 @ w, a64.abs() @ w.abs(), k, "last expert")
+
+
+@pytest.mark.parametrize("acc32", [False, True])
+def test_grouped_wgrad_output_past_4_gb(acc32):
+    g = gen(4)
+    e, m, n, blocks = 600, 2048, 4096, 3
+    a, sa = fb.fp8_quant_act_t(acts(g, 128 * blocks, m, 1e-3))
+    b, sb = fb.fp8_quant_act_t(acts(g, 128 * blocks, n))
+    seg = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    seg[-1] = blocks             # all for the last expert
+    if acc32:
+        d = torch.ones(e, m, n, device="cuda")
+        fb.fp8_gemm_grouped_wgrad_acc32(a, sa, b, sb, seg, m, n, 128 * blocks, d)
+        assert all(bool((x == 1).all()) for x in d[:-1].split(50))
+    else:
+        d = torch.ones(e, m, n, dtype=torch.bfloat16, device="cuda")
+        fb.fp8_gemm_grouped(fb.WGRAD, a, sa, b, sb, seg, m, n, 128 * blocks, out=d)
+        assert all(bool((x == 0).all()) for x in d[:-1].split(50))
+    a64, b64 = rows64(a, sa), rows64(b, sb)
+    ref, mag = a64 @ b64.t(), a64.abs() @ b64.abs().t()
+    if acc32:
+        # 1 + sum: the sum's own error, and one rounding of the total
+        check(d[-1], 1 + ref, sum_bound(128 * blocks) * mag + 2.0 ** -24 * (1 + ref.abs() + mag), "last expert")
+    else:
+        check_bf16(d[-1], ref, mag, 128 * blocks, "last expert")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_rows_past_2_gb(dtype):
+    t, e, k = 1 << 20, 1024 if dtype == torch.float32 else 1023, 2
+    x = torch.zeros(t, e, dtype=dtype, device="cuda")
+    rows = torch.tensor([0, 1, t // 2 + 1, t - 2, t - 1], device="cuda")
+    x[rows] = torch.randn(5, e, generator=gen(5), device="cuda").to(dtype)
+    w, ids = fb.fp8_moe_route(x, k, renorm=False)
+    few_w, few_ids = fb.fp8_moe_route(x[rows], k, renorm=False)
+    assert torch.equal(w[rows], few_w) and torch.equal(ids[rows], few_ids)
+    assert ids[2:t // 2].eq(torch.tensor([0, 1], device="cuda")).all() and w[2:t // 2].eq(1 / torch.tensor(float(e), device="cuda")).all()
+    dw = torch.ones(t, k, device="cuda")
+    dw[rows] = torch.randn(5, k, generator=gen(6), device="cuda")
+    dl = fb.fp8_moe_route_bwd(dw, w, ids, x, renorm=False)
+    few = fb.fp8_moe_route_bwd(dw[rows], few_w, few_ids, x[rows], renorm=False)
+    assert torch.equal(dl[rows], few)
+
+
+def test_plan_most_pairs():
+    # nearly 2^20 pairs: every step of the warps' runs
+    t, e, k = 130000, 16, 8
+    _, ids = fb.fp8_moe_route(torch.randn(t, e, generator=gen(7), device="cuda"), k)
+    seg, row, src = (x.long() for x in fb.fp8_moe_plan(ids, e))
+    flat, r = ids.reshape(-1).long(), row.reshape(-1)
+    pairs = torch.arange(t * k, device="cuda")
+    count = torch.bincount(flat, minlength=e)
+    assert torch.equal(seg[1:] - seg[:-1], (count + 127) // 128)
+    order = torch.sort(flat, stable=True).indices
+    place = torch.empty_like(order)
+    place[order] = pairs - (torch.cumsum(count, 0) - count)[flat[order]]
+    assert torch.equal(r, 128 * seg[flat] + place)
+    assert torch.equal(src[r], pairs) and int((src >= 0).sum()) == t * k
+
+
+def test_two_layers_of_many_tokens_at_once():
+    # kernels with one CTA per SM on two streams
+    states = [make(gen(20 + n), 40, 24, 4, 512, 384) for n in range(2)]
+    outs = [torch.empty_like(s[0]) for s in states]
+    ws = [torch.empty(fb.fp8_moe_few_workspace(40, 4, 512, 384), dtype=torch.uint8, device="cuda") for _ in states]
+    want = [fb.fp8_moe_few(*s).clone() for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(30):
+        for s, o, w, st in zip(states, outs, ws, streams):
+            with torch.cuda.stream(st):
+                fb.fp8_moe_few(*s, out=o, workspace=w)
+    torch.cuda.synchronize()
+    assert fb.fp8bw_last_device_error() == 0
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))

@@ -104,6 +104,31 @@ bool none_null(std::initializer_list<const void *> ptrs)
     return true;
 }
 
+// Bytes of one argument.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Whether no output shares a byte with an input or with another output: CTAs of one launch
+// read inputs while others store results already.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    const auto meet = [](const Span &a, const Span &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.bytes > 0 && b.bytes > 0 && x < y + uintptr_t(b.bytes) && y < x + uintptr_t(a.bytes);
+    };
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span *q = outs.begin(); q != o; ++q)
+            if (meet(*o, *q))
+                return false;
+        for (const Span &i : ins)
+            if (meet(*o, i))
+                return false;
+    }
+    return true;
+}
+
 bool experts_ok(int64_t E)
 {
     return E > 0 && E <= FP8BW_MAX_EXPERTS;
@@ -330,6 +355,9 @@ int fp8_linear_few(const void *x_bf16, const uint8_t *qw, const float *sw, void 
     const int sms = device_sms({x_bf16, qw, sw, y_bf16, workspace}, &st);
     if (sms < 0)
         return st;
+    if (!apart({{y_bf16, M * N * 2}, {workspace, fp8_linear_few_workspace(M, K)}},
+               {{x_bf16, M * K * 2}, {qw, N * K}, {sw, N / 128 * (K / 128) * 4}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_linear_few(x_bf16, int(M), qw, sw, y_bf16, N, K, workspace,
                                               static_cast<cudaStream_t>(stream), sms));
 }
@@ -347,6 +375,8 @@ int fp8_moe_route(const void *logits, int bf16, int64_t T, int64_t E, int64_t k,
     const int sms = device_sms({logits, weights, ids}, &st);
     if (sms < 0)
         return st;
+    if (!apart({{weights, T * k * 4}, {ids, T * k * 4}}, {{logits, T * E * (bf16 ? 2 : 4)}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_moe_route(logits, bf16 != 0, T, int(E), int(k), renorm != 0,
                                              weights, ids, static_cast<cudaStream_t>(stream), sms));
 }
@@ -365,6 +395,10 @@ int fp8_moe_route_bwd(const float *dweights, const float *weights, const int32_t
     const int sms = device_sms({dweights, weights, ids, logits, dlogits}, &st);
     if (sms < 0)
         return st;
+    if (!apart({{dlogits, T * E * (bf16 ? 2 : 4)}},
+               {{dweights, T * k * 4}, {weights, T * k * 4}, {ids, T * k * 4},
+                {logits, T * E * (bf16 ? 2 : 4)}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_moe_route_bwd(dweights, weights, ids, logits, bf16 != 0, T, int(E),
                                                  int(k), renorm != 0, dlogits,
                                                  static_cast<cudaStream_t>(stream), sms));
@@ -392,6 +426,10 @@ int fp8_moe_plan(const int32_t *ids, int64_t T, int64_t E, int64_t k, int32_t *s
     int st;
     if (device_sms({ids, seg, row, src, workspace}, &st) < 0)
         return st;
+    if (!apart({{seg, (E + 1) * 4}, {row, T * k * 4}, {src, fp8_moe_plan_rows(T, E, k) * 4},
+                {workspace, fp8_moe_plan_workspace(T, E, k)}},
+               {{ids, T * k * 4}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_moe_plan(ids, T, int(k), int(E), seg, row, src, workspace,
                                             static_cast<cudaStream_t>(stream)));
 }
@@ -411,6 +449,12 @@ int fp8_gemm_grouped(int mode, const uint8_t *a, const float *sa, const uint8_t 
     const int sms = device_sms({a, sa, b, sb, seg, d_bf16}, &st);
     if (sms < 0)
         return st;
+    const int64_t w = mode == FP8BW_WGRAD ? 1 : E;  // matrices of b
+    if (!apart({{d_bf16, (mode == FP8BW_WGRAD ? E : 1) * M * N * 2}},
+               {{a, M * K}, {sa, K / 128 * M * 4}, {b, w * N * K},
+                {sb, mode == FP8BW_WGRAD ? K / 128 * N * 4 : w * (N / 128) * (K / 128) * 4},
+                {seg, (E + 1) * 4}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_gemm_grouped(mode, a, sa, b, sb, d_bf16, seg, int(E), M, N, K,
                                                 static_cast<cudaStream_t>(stream), sms));
 }
@@ -429,6 +473,9 @@ int fp8_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_
     const int sms = device_sms({a, sa, b, sb, seg, dw32}, &st);
     if (sms < 0)
         return st;
+    if (!apart({{dw32, E * M * N * 4}}, {{a, M * K}, {sa, K / 128 * M * 4}, {b, N * K},
+                                        {sb, K / 128 * N * 4}, {seg, (E + 1) * 4}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_gemm_grouped_wgrad_acc32(a, sa, b, sb, dw32, seg, int(E), M, N, K,
                                                             static_cast<cudaStream_t>(stream), sms));
 }
@@ -452,6 +499,11 @@ int fp8_moe_few(const void *x_bf16, const uint8_t *w1, const float *s1, const ui
     const int sms = device_sms({x_bf16, w1, s1, w2, s2, ids, weights, y_bf16, workspace}, &st);
     if (sms < 0)
         return st;
+    if (!apart({{y_bf16, T * H * 2}, {workspace, fp8_moe_few_workspace(T, k, H, I)}},
+               {{x_bf16, T * H * 2}, {w1, E * 2 * I * H}, {s1, E * (2 * I / 128) * (H / 128) * 4},
+                {w2, E * H * I}, {s2, E * (H / 128) * (I / 128) * 4}, {ids, T * k * 4},
+                {weights, T * k * 4}}))
+        return FP8BW_EINVAL;
     return from_cuda(fp8bw::launch_moe_few(x_bf16, int(T), w1, s1, w2, s2, ids, weights, int(k),
                                            int(E), H, I, y_bf16, workspace,
                                            static_cast<cudaStream_t>(stream), sms));
@@ -461,7 +513,7 @@ const char *fp8bw_status_string(int status)
 {
     switch (status) {
     case FP8BW_OK: return "FP8BW_OK";
-    case FP8BW_EINVAL: return "FP8BW_EINVAL: null pointer or invalid mode";
+    case FP8BW_EINVAL: return "FP8BW_EINVAL: null pointer or invalid mode, or an output that overlaps another argument";
     case FP8BW_EALIGN: return "FP8BW_EALIGN: pointer not 16-byte aligned";
     case FP8BW_ESHAPE:
         return "FP8BW_ESHAPE: size not a positive multiple of 128 (16 for a token count), or too large";

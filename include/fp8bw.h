@@ -36,6 +36,8 @@
  *                scale arrays have ceil(tokens/128) rows.  The E8M0 entry points
  *                keep whole groups.  The few-token and mixture-of-experts calls state
  *                their own limits on tokens, experts and choices.
+ *   Overlap      No output or workspace may share memory with another argument.  The
+ *                few-token and mixture-of-experts calls check it (FP8BW_EINVAL).
  *   Alignment    Every pointer must be 16-byte aligned (else FP8BW_EALIGN).
  *   Streams      `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
  *                enqueued asynchronously; no call but fp8bw_last_device_error
@@ -67,7 +69,7 @@ extern "C" {
 
 typedef enum {
     FP8BW_OK = 0,
-    FP8BW_EINVAL = 1,      /* null pointer or bad mode */
+    FP8BW_EINVAL = 1,      /* null pointer or bad mode; an output that overlaps another argument */
     FP8BW_EALIGN = 2,      /* a pointer is not 16-byte aligned */
     FP8BW_ESHAPE = 3,      /* a size is not a positive multiple of 128 (16 for a token count), or too large */
     FP8BW_ECUDA = 4,       /* a CUDA runtime call or kernel launch failed */

@@ -167,3 +167,42 @@ def test_two_layers_of_many_tokens_at_once():
     torch.cuda.synchronize()
     assert fb.fp8bw_last_device_error() == 0
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_overlapping_arguments_are_refused():
+    # CTAs of one launch would read what others have stored
+    a = make(gen(30), 4, 8, 2, 256, 256)
+    x, w1, s1, w2, s2, ids, wt = a
+    square, scales = w2[0], s2[0]
+    logits = torch.randn(4, 8, generator=gen(31), device="cuda")
+    dw = torch.ones(4, 2, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    many = x.repeat(16, 1)
+    codes, sc = fb.fp8_quant_act(acts(gen(32), 256, 256))
+    seg = torch.tensor([0, 1, 2] + [2] * 6, dtype=torch.int32, device="cuda")
+    q, qs = fb.fp8_quant_act_t(acts(gen(33), 256, 256))
+    main = torch.zeros(1 << 21, device="cuda")
+    inside = main[:8 * 256 * 256].view(8, 256, 256)
+    for call in (
+            lambda: fb.fp8_linear_few(x, square, scales, out=x),
+            lambda: fb.fp8_linear_few(many, square, scales, out=ws[:64 * 256 * 2].view(torch.bfloat16).view(64, 256),
+                                      workspace=ws),
+            lambda: fb.fp8_moe_route(logits, 8, weights=logits),
+            lambda: fb.fp8_moe_route(logits, 2, weights=dw, ids=dw.view(torch.int32)),
+            lambda: fb.fp8_moe_route_bwd(dw, wt, ids, logits, dlogits=logits),
+            lambda: fb.fp8_moe_plan(ids, 8, row=ids),
+            lambda: fb.fp8_moe_plan(ids, 8, seg=ws[:36].view(torch.int32), workspace=ws),
+            lambda: fb.fp8_gemm_grouped(fb.FPROP, codes, sc, w2, s2, seg, 256, 256, 256,
+                                        out=w2.view(-1)[:256 * 256 * 2].view(torch.bfloat16).view(256, 256)),
+            lambda: fb.fp8_gemm_grouped_wgrad_acc32(q, qs, inside[0].view(torch.uint8).view(-1)[:65536].view(256, 256),
+                                                    qs, seg, 256, 256, 256, inside),
+            lambda: fb.fp8_moe_few(*a, out=x),
+            lambda: fb.fp8_moe_few(*a, workspace=w1.view(-1))):
+        with pytest.raises(fb.Fp8bwError) as e:
+            call()
+        assert e.value.status == 1
+    # neighbours in one buffer are apart
+    both = torch.empty(2, 4, 256, dtype=torch.bfloat16, device="cuda")
+    both[0] = x
+    y = fb.fp8_linear_few(both[0], square, scales, out=both[1])
+    assert torch.equal(y, fb.fp8_linear_few(x, square, scales))

@@ -155,76 +155,145 @@ __device__ __forceinline__ float exp_neg(float d)
     return r;
 }
 
-// What is left of a row, each lane's registers as in load_row: next() gives the largest
-// remaining logit and its expert, ties to the lowest, and takes it out; key 0 when none
-// is left.
+// The k largest logits of a row, each lane's registers as in Row; a lane's register holds a
+// word whose order is theirs.  Nothing has to be taken out between two rounds: relative
+// to the last maximum, counting down modulo 2^32, what is below it comes before what is
+// not.
+template <int NV> struct RowWords {
+    uint32_t word[NV], last;
+    // the next round's maximum distance, and this lane's
+    __device__ __forceinline__ uint32_t descend(uint32_t &mine)
+    {
+        mine = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            mine = max(mine, word[i] - last);
+        const uint32_t far = __reduce_max_sync(0xffffffffu, mine);
+        last += far;
+        return far;
+    }
+};
+
+// choose() gives lane j the key of choice j (0: none), and every lane that of the first.
+// Lane j has its id where OWN_ID is set; otherwise choose() has stored the row's ids.
 //
 // BF16 logits: value and expert fit one word, (16-bit order key, ~expert), so that words
-// are distinct and one warp-wide maximum (redux) finds both.  Nothing has to be taken
-// out: relative to the last maximum, counting down modulo 2^32, what is below it comes
-// before what is not.
-template <class T, int V, int NV> struct RowTop {
-    uint32_t word[NV], last;
-    __device__ __forceinline__ void init(const float (&v)[NV], int lane)
+// are distinct and one warp-wide maximum (redux) finds both.
+template <class T, int V, int NV> struct RowTop : RowWords<NV> {
+    static constexpr bool OWN_ID = true;
+    __device__ __forceinline__ int choose(const float (&v)[NV], int k, int lane, int32_t *,
+                                          uint32_t &key, uint32_t &top)
     {
-        last = 0u;
+        this->last = 0u;
         const uint32_t first = 0xFFFFu - uint32_t(expert_of<V>(0, lane));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t u = __float_as_uint(__fadd_rn(v[i], 0.0f));
-            const uint32_t key = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-            word[i] = (key & 0xFFFF0000u) | (first - uint32_t(expert_of<V>(i, 0)));
+            const uint32_t order = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+            this->word[i] = (order & 0xFFFF0000u) | (first - uint32_t(expert_of<V>(i, 0)));
         }
+        uint32_t mine = next(), top_word = mine;  // lane j: word of choice j, in the end
+        int left = 1;
+        for (int j = 1; j < k; ++j) {
+            const uint32_t w = next();
+            if (w == 0u)
+                break;
+            mine = lane >= j ? w : mine;
+            left = j + 1;
+        }
+        top = key_of(top_word);
+        key = lane < left ? key_of(mine) : 0u;
+        return key ? int(0xFFFFu - (mine & 0xFFFFu)) : -1;
     }
     // The next word, 0 when none is left (-inf has the lowest key, 0x007F).
     __device__ __forceinline__ uint32_t next()
     {
-        uint32_t best = 0u;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            best = max(best, word[i] - last);
-        last += __reduce_max_sync(0xffffffffu, best);
-        return last >= 0x00800000u ? last : 0u;
+        uint32_t unused;
+        this->descend(unused);
+        return this->last >= 0x00800000u ? this->last : 0u;
     }
     // (the low half of a BF16 value's key is all its sign's)
     __device__ __forceinline__ static uint32_t key_of(uint32_t w)
     {
         return w == 0u ? 0u : (w >> 31) ? w & 0xFFFF0000u : w | 0xFFFFu;
     }
-    __device__ __forceinline__ static int expert(uint32_t w) { return int(0xFFFFu - (w & 0xFFFFu)); }
 };
 
-// FP32 logits: a maximum of the values, then the lowest expert that has it.  A choice is
-// a 64-bit word, (key, ~expert).
-template <int V, int NV> struct RowTop<float, V, NV> {
-    uint32_t left[NV];
-    uint32_t first;  // expert of register 0
-    __device__ __forceinline__ void init(const float (&v)[NV], int lane)
+// FP32 logits: the rounds find the k largest keys, each lane noting the rounds that it won;
+// which register it was is looked up afterwards, once per lane and win (two or three times,
+// in place of k).  Equal logits among the choices show in there being more registers of at
+// least the last key than rounds; then the rounds are done again, one expert at a time.
+template <int V, int NV> struct RowTop<float, V, NV> : RowWords<NV> {
+    static constexpr bool OWN_ID = false;
+    __device__ __forceinline__ int choose(const float (&v)[NV], int k, int lane, int32_t *ids,
+                                          uint32_t &key, uint32_t &top)
     {
-        first = uint32_t(expert_of<V>(0, lane));
+        uint32_t(&word)[NV] = this->word;
+        const uint32_t first = uint32_t(expert_of<V>(0, lane));
+        this->last = 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            left[i] = order_key(v[i]);
-    }
-    __device__ __forceinline__ uint64_t next()
-    {
-        uint32_t best = left[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i)
-            best = max(best, left[i]);
-        const uint32_t key = __reduce_max_sync(0xffffffffu, best);
-        uint32_t mine = 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-            mine = left[i] == key ? first + uint32_t(expert_of<V>(i, 0)) : mine;
-        const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+            word[i] = order_key(v[i]);
+        uint32_t mine = 0u, wins = 0u, last = 0u;
+        int left = 0;
+        for (; left < k; ++left) {
+            uint32_t best;
+            const uint32_t far = this->descend(best);
+            if (this->last == 0u)
+                break;
+            last = this->last;
+            mine = lane >= left ? last : mine;
+            wins |= best == far ? 1u << left : 0u;
+        }
+        int count = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            left[i] = e - first == uint32_t(expert_of<V>(i, 0)) ? 0u : left[i];
-        return key ? uint64_t(key) << 32 | e : 0u;
+            count += word[i] >= last;
+        if (left == 0 || __reduce_add_sync(0xffffffffu, count) == left) {
+            if (lane >= left && lane < k)
+                ids[lane] = -1;
+            while (__any_sync(0xffffffffu, wins != 0u)) {
+                const int j = __ffs(wins) - 1;
+                const uint32_t want = __shfl_sync(0xffffffffu, mine, j & 31);
+                uint32_t e = 0u;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    e = word[i] == want ? uint32_t(expert_of<V>(i, 0)) : e;
+                if (wins)
+                    ids[j] = int32_t(first + e);
+                wins &= wins - 1u;
+            }
+        } else {
+            left = 0;
+            int id = -1;
+            for (; left < k; ++left) {
+                uint32_t best = word[0];
+#pragma unroll
+                for (int i = 1; i < NV; ++i)
+                    best = max(best, word[i]);
+                const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+                if (high == 0u)
+                    break;
+                uint32_t lowest = 0xFFFFFFFFu;
+#pragma unroll
+                for (int i = NV - 1; i >= 0; --i)
+                    lowest = word[i] == high ? first + uint32_t(expert_of<V>(i, 0)) : lowest;
+                const uint32_t e = __reduce_min_sync(0xffffffffu, lowest);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    word[i] = e - first == uint32_t(expert_of<V>(i, 0)) ? 0u : word[i];
+                if (lane == left) {
+                    mine = high;
+                    id = int(e);
+                }
+            }
+            if (lane < k)
+                ids[lane] = id;
+        }
+        key = lane < left ? mine : 0u;
+        top = __shfl_sync(0xffffffffu, key, 0);
+        return -1;
     }
-    __device__ __forceinline__ static uint32_t key_of(uint64_t w) { return uint32_t(w >> 32); }
-    __device__ __forceinline__ static int expert(uint64_t w) { return int(uint32_t(w)); }
 };
 
 // weights[t][j], ids[t][j] for the k largest logits of row t, largest first, ties to
@@ -250,20 +319,8 @@ moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int r
         if (t + step < rows)
             next.load(logits + (t + step) * E, E, lane);
         RowTop<T, V, NV> row;
-        row.init(v, lane);
-        auto mine = row.next();  // lane j: choice j, in the end
-        const auto top_word = mine;
-        int left = 1;  // choices there are
-        for (int j = 1; j < k; ++j) {
-            const auto w = row.next();
-            if (w == 0u)  // nothing is left: this choice and the later ones stay empty
-                break;
-            mine = lane >= j ? w : mine;
-            left = j + 1;
-        }
-        const uint32_t top_key = row.key_of(top_word);
-        const uint32_t my_key = lane < left ? row.key_of(mine) : 0u;
-        const int my_id = my_key ? row.expert(mine) : -1;
+        uint32_t my_key, top_key;
+        const int my_id = row.choose(v, k, lane, ids + t * k, my_key, top_key);
         const float top = key_value(top_key);
         const float p = my_key ? exp_neg(key_value(my_key) - top) : 0.0f;
         float s = p;
@@ -278,7 +335,8 @@ moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int r
         const float den = warp_sum(s);
         if (lane < k) {
             weights[t * k + lane] = my_key ? p / den : 0.0f;
-            ids[t * k + lane] = my_id;
+            if (row.OWN_ID)
+                ids[t * k + lane] = my_id;
         }
     }
 }

@@ -2,8 +2,8 @@
 // weights, the gradient of the logits, and the plan that lays the chosen (token,
 // expert) pairs out by expert for the grouped GEMM.
 //
-// All three are bound by memory latency at small sizes and by issue slots at large
-// ones; the bytes they move are small next to the layer's products.
+// All three are bound by latency at small sizes and by issue slots at large ones; the
+// bytes they move are small next to the layer's products.
 #include <cfloat>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -298,7 +298,11 @@ template <int V, int NV> struct RowTop<float, V, NV> : RowWords<NV> {
 
 // weights[t][j], ids[t][j] for the k largest logits of row t, largest first, ties to
 // the lowest expert.  One warp per token, k rounds of RowTop; lane j keeps choice j.
-// Statistics in FP32.  Bound by issue slots: about 2 NV + 12 instructions a round.
+// Statistics in FP32.  Bound by the integer unit (71% busy at 65521 x 256 with 8 choices): a
+// round takes a subtraction and a maximum per register.  That size takes 27.0 us in BF16
+// (1.4 TB/s) and 38.7 us in FP32 (1.8 TB/s), whose registers are twice the bytes; 8192 x 128
+// in FP32 5.5 us.  (A warp per row: half a warp would save nothing, the registers' work
+// being the same.)  Tried: differences by multiply-adds and maxima of three, 30.5 us.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int renorm,
@@ -346,7 +350,9 @@ moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int r
 // expert p is its weight, so that the element is w_j (dw_j - G).  Every element of the row
 // is written, first the row without its choices, then these.  A choice with an id
 // outside [0, E) takes no part.  One warp per token, in FP32, rounded once to the logits'
-// type.  Bound by HBM: the row written, and read for the softmax over all.
+// type.  The row written, and read for the softmax over all: 65521 x 256 with 8 choices in
+// FP32 24.8 us (5.7 TB/s) and 18.9 us renormalized (3.9 TB/s); in BF16 20.8 and 15.0 us, bound
+// by issue slots (the exponentials and the row's way through shared memory).
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict__ weights,
@@ -462,18 +468,24 @@ moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict
 // Counting the ids of every run gives, by prefix sums over warps and chunks, the place at
 // which each run's first pair of an expert goes; inside a run a warp ranks 32 pairs at a
 // time by matching ids.  All sums are of whole numbers, and a pair's place depends on the
-// ids alone.  Every CTA adds up all chunks' counts for itself, so there are few chunks.
+// ids alone.
+//
+// Bound by latency: the ids, the counts of the other chunks and the stores follow each
+// other; with many pairs per SM by the stores to src, a line for each pair.  So few
+// pairs go to one launch, a cluster whose CTAs read each other's counts, and more than
+// 2^15 to two launches of up to 64 CTAs, the first of which counts (one / two launches, us:
+// 16384 pairs 6.6 / 9.4, 32768 pairs 7.5 / 8.9, 65536 pairs 11.0 / 9.1; 30 pairs take 4.5,
+// 524168 pairs over 256 experts 15.0).  Ranking in the counting pass, so that the rows
+// need no further votes, gains 0.4 us at 30 pairs and loses 3.9 at 524168, where the votes
+// then no longer run under the stores.
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
 constexpr int PLAN_PAIRS = 2048;  // pairs of a chunk, at least
 constexpr int PLAN_CHUNKS = 64;
+constexpr int PLAN_CLUSTER = 8;   // chunks that one cluster takes, at most
 constexpr int PLAN_REGS = 16;     // 32-pair steps of a warp's run, at most
+constexpr int PLAN_CLUSTER_PAIRS = 1 << 15;  // pairs that one cluster takes, at most
 
-static int plan_chunks(int64_t pairs)
-{
-    const int64_t c = (pairs + PLAN_PAIRS - 1) / PLAN_PAIRS;
-    return int(c < 1 ? 1 : c > PLAN_CHUNKS ? PLAN_CHUNKS : c);
-}
 // (the layout holds at most 2^20 rows, and so pairs)
 static_assert(int64_t(PLAN_CHUNKS) * PLAN_WARPS * PLAN_REGS * 32 >= (1 << 20), "runs hold all pairs");
 
@@ -495,7 +507,7 @@ struct PlanRun {
             id[i] = v >= 0 && v < E ? v : -1;
         }
     }
-    // Adds them to cnt[E] (shared, this warp's own).
+    // Adds them to cnt[E] (shared).
     __device__ __forceinline__ void count(int *cnt) const
     {
 #pragma unroll
@@ -523,6 +535,16 @@ moe_plan_count_kernel(const int32_t *__restrict__ ids, int pairs, int E, int *__
         hist[e * PLAN_CHUNKS + blockIdx.x] = cnt[e];
 }
 
+__device__ __forceinline__ int ld_cluster_int(const int *p, int rank)
+{
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), uint32_t(rank))) : "memory");
+    return v;
+}
+
+// CLUSTER: the chunks are the CTAs of one cluster and read each other's counts from shared
+// memory; otherwise the counts of all chunks come from moe_plan_count_kernel.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(PLAN_THREADS)
 moe_plan_place_kernel(const int32_t *__restrict__ ids, int pairs, int E,
                       const int *__restrict__ hist, int rows, int32_t *__restrict__ seg,
@@ -530,24 +552,28 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int pairs, int E,
 {
     extern __shared__ int sh[];
     int *cnt = sh;                      // [PLAN_WARPS][E]
-    int *total = cnt + PLAN_WARPS * E;  // [E]
-    int *before = total + E;            // [E] pairs of the expert in earlier chunks
-    int *first = before + E;            // [E + 1] first block of the expert
+    int *own = cnt + PLAN_WARPS * E;    // [E] this chunk's pairs of the expert
+    int *total = own + E;               // [E] all chunks'
+    int *base = total + E;              // [E] those of earlier chunks; then the chunk's first row
+    int *first = base + E;              // [E + 1] first block of the expert
+    __shared__ int warp_blocks[PLAN_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunk = blockIdx.x, chunks = gridDim.x;
-    for (int i = threadIdx.x; i < (PLAN_WARPS + 2) * E; i += PLAN_THREADS)
-        sh[i] = 0;
+    const int e = threadIdx.x;  // the expert that this thread sums up, if there is one
+    static_assert(PLAN_THREADS >= 1024, "a thread per expert");
+    for (int i = threadIdx.x; i < PLAN_WARPS * E; i += PLAN_THREADS)
+        cnt[i] = 0;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     PlanRun run;
     run.load(ids, pairs, E, chunk, chunks, warp, lane);
     run.count(cnt + warp * E);
-    if (chunks > 1) {
+    if (!CLUSTER) {
         // all chunks' counts, one warp per expert
 #pragma unroll 4
-        for (int e = warp; e < E; e += PLAN_WARPS) {
-            const int *h = hist + e * PLAN_CHUNKS;
+        for (int x = warp; x < E; x += PLAN_WARPS) {
+            const int *h = hist + x * PLAN_CHUNKS;
             int t = 0, b = 0;
 #pragma unroll
             for (int i = 0; i < PLAN_CHUNKS / 32; ++i) {
@@ -559,47 +585,64 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int pairs, int E,
             t = __reduce_add_sync(0xffffffffu, t);
             b = __reduce_add_sync(0xffffffffu, b);
             if (lane == 0) {
-                total[e] = t;
-                before[e] = b;
+                total[x] = t;
+                base[x] = b;
             }
         }
     }
     __syncthreads();
-    // counts of each warp's run -> where the run's first pair of each expert goes
-    for (int e = threadIdx.x; e < E; e += PLAN_THREADS) {
-        int s = before[e];
+    // counts of each warp's run -> how many pairs of the expert come before it in the chunk
+    int all = 0, before = 0;
+    if (e < E) {
 #pragma unroll 8
         for (int w = 0; w < PLAN_WARPS; ++w) {
             const int c = cnt[w * E + e];
-            cnt[w * E + e] = s;
-            s += c;
+            cnt[w * E + e] = all;
+            all += c;
         }
-        if (chunks == 1)
-            total[e] = s;
+        own[e] = all;
     }
-    __syncthreads();
-    if (warp == 0) {  // blocks of each expert, summed over the experts before it
-        int carry = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            const int b = e < E ? (total[e] + 127) / 128 : 0;
-            int s = b;
+    if (CLUSTER) {
+        cluster_sync();
+        if (e < E) {
+            int n[PLAN_CLUSTER];
+            all = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, s, o);
-                s += lane >= o ? up : 0;
+            for (int c = 0; c < PLAN_CLUSTER; ++c)
+                n[c] = c < chunks ? ld_cluster_int(own + e, c) : 0;
+#pragma unroll
+            for (int c = 0; c < PLAN_CLUSTER; ++c) {
+                all += n[c];
+                before += c < chunk ? n[c] : 0;
             }
-            if (e < E)
-                first[e] = carry + s - b;
-            carry += __shfl_sync(0xffffffffu, s, 31);
+            total[e] = all;
         }
-        if (lane == 0)
-            first[E] = carry;
+    } else if (e < E) {
+        all = total[e];
+        before = base[e];
+    }
+    // blocks of each expert, summed over the experts before it
+    const int blocks = e < E ? (all + 127) / 128 : 0;
+    int sum = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        sum += lane >= o ? up : 0;
+    }
+    if (lane == 31)
+        warp_blocks[warp] = sum;
+    __syncthreads();
+    sum += __reduce_add_sync(0xffffffffu, lane < warp ? warp_blocks[lane] : 0);
+    if (e < E) {
+        first[e] = sum - blocks;
+        base[e] = (sum - blocks) * 128 + before;
+        if (e == E - 1)
+            first[E] = sum;
     }
     __syncthreads();
     if (chunk == 0)
-        for (int e = threadIdx.x; e <= E; e += PLAN_THREADS)
-            seg[e] = first[e];
+        for (int i = threadIdx.x; i <= E; i += PLAN_THREADS)
+            seg[i] = first[i];
     int *mine = cnt + warp * E;
 #pragma unroll
     for (int i = 0; i < PLAN_REGS; ++i) {
@@ -616,35 +659,42 @@ moe_plan_place_kernel(const int32_t *__restrict__ ids, int pairs, int E,
             mine[id] = at + 1;
         __syncwarp();
         if (p < run.hi) {
-            const int r = id >= 0 ? first[id] * 128 + at : -1;
+            const int r = id >= 0 ? base[id] + at : -1;
             row[p] = r;
             if (r >= 0)
                 src[r] = p;
         }
     }
     // rows that no pair takes: the rest of each expert's last block, and all behind the last
-    for (int e = chunk * PLAN_WARPS + warp; e < E; e += chunks * PLAN_WARPS)
-        for (int r = first[e] * 128 + total[e] + lane; r < first[e + 1] * 128; r += 32)
+    for (int x = chunk * PLAN_WARPS + warp; x < E; x += chunks * PLAN_WARPS)
+        for (int r = first[x] * 128 + total[x] + lane; r < first[x + 1] * 128; r += 32)
             src[r] = -1;
     for (int r = first[E] * 128 + chunk * PLAN_THREADS + threadIdx.x; r < rows;
          r += chunks * PLAN_THREADS)
         src[r] = -1;
+    if (CLUSTER)
+        cluster_sync();  // no peer reads this CTA's counts any more
 }
 
 // ------------------------------------------------------------------- host side
 
 template <class K, class... A>
-static cudaError_t launch(K kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+static cudaError_t launch(K kern, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                          A... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     set_pdl(at[0]);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = unsigned(cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -683,7 +733,7 @@ static cudaError_t route(const void *logits, int64_t rows, int E, int k, bool re
     return with_layout<T>(E, [&](auto l) {
         using L = decltype(l);
         return launch(moe_route_kernel<T, L::V, L::NV>, route_grid(rows, num_sms), ROUTE_WARPS * 32,
-                      0, stream, static_cast<const T *>(logits), rows, E, k, int(renorm), weights,
+                      0, 1, stream, static_cast<const T *>(logits), rows, E, k, int(renorm), weights,
                       ids);
     });
 }
@@ -696,7 +746,7 @@ static cudaError_t route_bwd(const float *dweights, const float *weights, const 
     return with_layout<T>(E, [&](auto l) {
         using L = decltype(l);
         return launch(moe_route_bwd_kernel<T, L::V, L::NV>, route_grid(rows, num_sms),
-                      ROUTE_WARPS * 32, 0, stream, dweights, weights, ids,
+                      ROUTE_WARPS * 32, 0, 1, stream, dweights, weights, ids,
                       static_cast<const T *>(logits), rows, E, k, int(renorm),
                       static_cast<T *>(dlogits));
     });
@@ -734,30 +784,38 @@ cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t
                             int32_t *row, int32_t *src, void *workspace, cudaStream_t stream)
 {
     const int pairs = int(T * k);
-    const int chunks = plan_chunks(pairs);
+    const bool one = pairs <= PLAN_CLUSTER_PAIRS;  // one cluster
+    const int64_t wanted = (pairs + PLAN_PAIRS - 1) / PLAN_PAIRS, most = one ? PLAN_CLUSTER : PLAN_CHUNKS;
+    const int chunks = int(wanted < most ? wanted : most);
     const size_t count_smem = size_t(E) * sizeof(int);
-    const size_t place_smem = ((PLAN_WARPS + 3) * size_t(E) + 1) * sizeof(int);
+    const size_t place_smem = ((PLAN_WARPS + 4) * size_t(E) + 1) * sizeof(int);
     static LaunchCache cache;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (cache.get(dev) == 0) {
-        e = cudaFuncSetAttribute(moe_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 ((PLAN_WARPS + 3) * 1024 + 1) * int(sizeof(int)));
+        constexpr int most_smem = ((PLAN_WARPS + 4) * 1024 + 1) * int(sizeof(int));
+        e = cudaFuncSetAttribute(moe_plan_place_kernel<true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(moe_plan_place_kernel<false>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
         if (e != cudaSuccess)
             return e;
         cache.set(dev, 1);
     }
+    const int rows = int(moe_plan_rows(T, k, E));
     int *hist = static_cast<int *>(workspace);
-    if (chunks > 1) {
-        e = launch(moe_plan_count_kernel, dim3(chunks), PLAN_THREADS, count_smem, stream, ids, pairs,
-                   E, hist);
-        if (e != cudaSuccess)
-            return e;
-    }
-    return launch(moe_plan_place_kernel, dim3(chunks), PLAN_THREADS, place_smem, stream, ids, pairs,
-                  E, static_cast<const int *>(hist), int(moe_plan_rows(T, k, E)), seg, row, src);
+    if (one)
+        return launch(moe_plan_place_kernel<true>, dim3(chunks), PLAN_THREADS, place_smem, chunks,
+                      stream, ids, pairs, E, static_cast<const int *>(hist), rows, seg, row, src);
+    e = launch(moe_plan_count_kernel, dim3(chunks), PLAN_THREADS, count_smem, 1, stream, ids, pairs, E,
+               hist);
+    if (e != cudaSuccess)
+        return e;
+    return launch(moe_plan_place_kernel<false>, dim3(chunks), PLAN_THREADS, place_smem, 1, stream, ids,
+                  pairs, E, static_cast<const int *>(hist), rows, seg, row, src);
 }
 
 } // namespace fp8bw

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import blockwise_fp8_linear_b200 as fb
-from _moe import acts, blocks64, check, check_bf16, dequant_rows, layer, rows64, sum_bound, weights
+from _moe import U32, acts, blocks64, check, check_bf16, dequant_rows, layer, rows64, route, sum_bound, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -136,20 +136,42 @@ def test_route_rows_past_2_gb(dtype):
     assert torch.equal(dl[rows], few)
 
 
-def test_plan_most_pairs():
-    # nearly 2^20 pairs: every step of the warps' runs
-    t, e, k = 130000, 16, 8
-    _, ids = fb.fp8_moe_route(torch.randn(t, e, generator=gen(7), device="cuda"), k)
+@pytest.mark.parametrize("t,e,k,out", [
+    (130000, 16, 8, False),   # nearly 2^20 pairs: every step of the warps' runs
+    (300, 1024, 8, True), (1021, 1000, 16, True), (2341, 7, 7, True), (1 << 15, 1, 1, False),
+    (4096, 64, 8, True), (4097, 64, 8, True)])   # 2^15 pairs and a token more
+def test_plan_of_many_pairs(t, e, k, out):
+    g = gen(7)
+    _, ids = fb.fp8_moe_route(torch.randn(t, e, generator=g, device="cuda"), k)
+    if out:
+        ids[torch.rand(t, k, generator=g, device="cuda") < 0.1] = -1
+        ids[3] = e
     seg, row, src = (x.long() for x in fb.fp8_moe_plan(ids, e))
     flat, r = ids.reshape(-1).long(), row.reshape(-1)
-    pairs = torch.arange(t * k, device="cuda")
+    pairs = torch.nonzero((flat >= 0) & (flat < e)).view(-1)
+    flat = flat[pairs]
     count = torch.bincount(flat, minlength=e)
-    assert torch.equal(seg[1:] - seg[:-1], (count + 127) // 128)
+    assert int(seg[0]) == 0 and torch.equal(seg[1:] - seg[:-1], (count + 127) // 128)
     order = torch.sort(flat, stable=True).indices
     place = torch.empty_like(order)
-    place[order] = pairs - (torch.cumsum(count, 0) - count)[flat[order]]
-    assert torch.equal(r, 128 * seg[flat] + place)
-    assert torch.equal(src[r], pairs) and int((src >= 0).sum()) == t * k
+    place[order] = torch.arange(len(order), device="cuda") - (torch.cumsum(count, 0) - count)[flat[order]]
+    assert torch.equal(r[pairs], 128 * seg[flat] + place) and int((r >= 0).sum()) == len(pairs)
+    assert torch.equal(src[r[pairs]], pairs) and int((src >= 0).sum()) == len(pairs)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t,e,k", [(65, 7, 7), (130, 64, 8), (130, 256, 32), (67, 1000, 5), (65, 1024, 32)])
+def test_route_among_few_values(t, e, k, dtype):
+    # equal logits within a lane, across lanes, and around the last choice
+    g = gen(e)
+    levels = torch.randint(1, 2 * e, (t, 1), generator=g, device="cuda")
+    x = (torch.randint(0, 1 << 20, (t, e), generator=g, device="cuda") % levels / 64).to(dtype)
+    x[torch.rand(t, e, generator=g, device="cuda") < 0.2] = -torch.inf
+    w, ids = fb.fp8_moe_route(x, k)
+    ref_ids, ref_w, _ = route(x, k, True)
+    assert torch.equal(ids.long(), ref_ids)
+    # exp to 2 ulp, its argument within |d| 2^-24, |d| <= 32; k + 1 sums and a division
+    check(w, ref_w, (64 + k) * U32 * ref_w + 2.0 ** -126, "weights")
 
 
 def test_two_layers_of_many_tokens_at_once():

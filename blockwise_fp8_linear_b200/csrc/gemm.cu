@@ -1017,7 +1017,13 @@ cudaError_t launch_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uin
 }
 
 // Grouped GEMM: how many rows each expert has is known to the GPU alone, so the tile is
-// chosen by what the sizes lead to expect.
+// chosen by what the sizes lead to expect.  Large ones are bound as the dense GEMM is, by the
+// promotion of each block's partial sums, and compute the rows that fill each expert's last
+// block as well: fprop of 65536 pairs, 128 experts, N 1536, K 2048, 340 us (1.2 PFLOP/s of
+// the pairs' products; an eighth as many rows again are fill); dgrad of 16384 pairs, 32 experts, N 1024, K
+// 2048, 65 us; wgrad of 32768 pairs, 32 experts, 2048 x 1536, 235 us, each tile with a
+// reduction of 8 blocks on average and a reduce-add of 256 KB into L2 behind it.  Small ones
+// are bound by latency (1000 pairs, 16 experts, N = K = 1024: 8.5 us, 16.5 MB).
 //
 // fprop, dgrad: each expert's last block is half full on average, so the blocks in use are
 // those there are less half an expert's each, and pairs of blocks waste another quarter

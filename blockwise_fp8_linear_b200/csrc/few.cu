@@ -679,26 +679,44 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         }
     } else if (Cfg::EXPERTS && warp >= Cfg::FIN_WARP0) {
         // --------------------------------------------------------- finish the rows
+        // Rows go to the warps in turn, on from the item before: most items have fewer rows
+        // than there are warps, and a row of down takes about as long as an item's products.
+        constexpr int FIN = Cfg::FIN_WARPS > 0 ? Cfg::FIN_WARPS : 1;
         Walk at;
-        for (int item = first, m = 0; item < items && split == 1; item += step, ++m) {
+        for (int item = first, m = 0, turn = 0; item < items && split == 1; item += step, ++m) {
             enter(at, item);
-            const int rb = m % Cfg::RBUF;
+            const int rb = m % Cfg::RBUF, rows = at.u.rows;
             const bool ok = mbar_wait_bounded(&rfull[rb], uint32_t(m / Cfg::RBUF) & 1u, abort_flag,
                                               &g_few_error, FERR_FINISH, FEW_WAIT_NS);
             if (!__all_sync(0xffffffffu, ok))
                 break;
-            for (int r = warp - Cfg::FIN_WARP0; r < at.u.rows; r += Cfg::FIN_WARPS) {
-                const float4 v = *reinterpret_cast<const float4 *>(red + (rb * NT + r) * 128 + 4 * lane);
-                if (KIND == FEW_UP)
-                    few_store_h(a, at.u.base + r, at.tile, lane, v);
-                else if (KIND == FEW_DOWN)
-                    few_combine(a, plan, at.u.base + r, at.tile, lane, v);
-                else
-                    few_store(a, r, at.tile, lane, v);
+            int r = warp - Cfg::FIN_WARP0 - turn;
+            r += r < 0 ? FIN : 0;
+            turn = (turn + rows) % FIN;
+            const float *sums = red + rb * NT * 128 + 4 * lane;
+            if (KIND == FEW_DOWN) {
+                // all of this warp's sums first: the buffer is free before the rows are done
+                constexpr int MINE = (NT + FIN - 1) / FIN;
+                float4 v[MINE];
+#pragma unroll
+                for (int i = 0; i < MINE; ++i)
+                    if (r + i * FIN < rows)
+                        v[i] = *reinterpret_cast<const float4 *>(sums + (r + i * FIN) * 128);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&rempty[rb]);
+#pragma unroll
+                for (int i = 0; i < MINE; ++i)
+                    if (r + i * FIN < rows)
+                        few_combine(a, plan, at.u.base + r + i * FIN, at.tile, lane, v[i]);
+            } else {
+                for (; r < rows; r += FIN)
+                    few_store_h(a, at.u.base + r, at.tile, lane,
+                                *reinterpret_cast<const float4 *>(sums + r * 128));
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&rempty[rb]);
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&rempty[rb]);
         }
     } else if (Cfg::QUANT) {
         // -------------------------------------------- quantize the tokens' groups

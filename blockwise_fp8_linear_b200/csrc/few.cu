@@ -36,13 +36,15 @@
 // Measured on the device, weights from HBM (one B200, 6.5 TB/s copy rate):
 //   linear  1 token 2048 x 2048 4.4 us; 7 tokens 2048 x 6144 7.2 us; 8 tokens 12288 x 2048
 //           9.4 us (2.7 TB/s); 1 token 12288 x 12288 28.8 us (5.3 TB/s)
-//   codes   61 tokens 12288 x 2048 14.9 us with the quantizer's launch (1.8 TB/s: 96 tiles on
-//           148 SMs); 64 tokens 12288 x 12288 46.7 us (3.3 TB/s)
+//   codes   61 tokens 12288 x 2048 13.8 us with the quantizer's launch (2.0 TB/s: 96 tiles on
+//           148 SMs); 64 tokens 12288 x 12288 42.8 us (3.6 TB/s)
 //   layer   128 experts of 2048 x 768, 8 choices: 1 token 21.8 us (start-up, join and
-//           combination are most of it); 8 tokens 61 us (4.0 TB/s); 40 tokens 115 us (4.9
-//           TB/s), up about 63 of it (57 at the copy rate); 64 tokens 132 us (4.5 TB/s)
-// The layer of many tokens is bound by HBM and by uneven ends: an SM takes whole items, so
-// that up's SMs are done between 49 and 69 us at 40 tokens.
+//           combination are most of it); 8 tokens 59 us (4.0 TB/s); 40 tokens 111 us (5.1
+//           TB/s); 64 tokens 128 us (4.7 TB/s)
+// The layer of many tokens is bound by HBM and by starts and ends.  At 40 tokens up's first
+// product is done after 11 us (the tokens' groups wait behind the first weights), and as an
+// SM takes whole items, 4.8 of them on average, up's SMs end between 59 and 77 us; down,
+// which may only multiply once all have, ends at 113 to 115.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -768,19 +770,56 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
         }
     } else {
         // --------------------------------------------------- scales of the codes
-        pdl_wait();
+        // A few blocks at a time, the next ones' under way meanwhile: one after the other,
+        // each block would wait for memory anew (61 tokens, 12288 x 2048: 14.9 us so, 13.8 by
+        // four; 64 tokens, 12288 x 12288: 46.6 and 42.8).  Down of up to 16 tokens has the
+        // registers for one ahead.
+        constexpr int G = Cfg::EXPERTS && Cfg::BLOCKS == 2 ? 1 : 4, PER = (NT + 31) / 32;
+        // loads those of the G blocks from `from` on, and returns the place behind them
+        const auto fetch = [&](Walk from, float (&v)[G][PER]) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (from.item < items && lane + 32 * q < from.u.rows)
+                        v[g][q] = a.sx[size_t(lo + from.i) * a.sx_rows + from.u.base + lane + 32 * q];
+                if (from.item < items)
+                    advance(from, 1);
+            }
+            return from;
+        };
+        float v[G][PER], ahead[G][PER];
         Walk w = start(0);
-        for (int n = 0; w.item < items; ++n, advance(w, 1)) {
-            const int s = n % STAGES;
-            const bool ok = mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
-                                              &g_few_error, FERR_ACT, FEW_WAIT_NS);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
-            for (int r = lane; r < w.u.rows; r += 32)
-                xs[s * NT + r] = a.sx[size_t(lo + w.i) * a.sx_rows + w.u.base + r];
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&full[s]);
+        pdl_wait();
+        Walk next = fetch(w, v);
+        bool ok = true;
+        for (int n = 0; w.item < items && ok;) {
+            next = fetch(next, ahead);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (w.item >= items)
+                    break;
+                const int s = n % STAGES;
+                ok = mbar_wait_bounded(&empty[s], (uint32_t(n / STAGES) & 1u) ^ 1u, abort_flag,
+                                       &g_few_error, FERR_ACT, FEW_WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    if (lane + 32 * q < w.u.rows)
+                        xs[s * NT + lane + 32 * q] = v[g][q];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&full[s]);
+                advance(w, 1);
+                ++n;
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    v[g][q] = ahead[g][q];
         }
     }
     if (!Cfg::QUANT)

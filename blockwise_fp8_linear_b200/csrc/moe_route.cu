@@ -471,20 +471,21 @@ moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict
 // ids alone.
 //
 // Bound by latency: the ids, the counts of the other chunks and the stores follow each
-// other; with many pairs per SM by the stores to src, a line for each pair.  So few
-// pairs go to one launch, a cluster whose CTAs read each other's counts, and more than
-// 2^15 to two launches of up to 64 CTAs, the first of which counts (one / two launches, us:
-// 16384 pairs 6.6 / 9.4, 32768 pairs 7.5 / 8.9, 65536 pairs 11.0 / 9.1; 30 pairs take 4.5,
-// 524168 pairs over 256 experts 15.0).  Ranking in the counting pass, so that the rows
+// other; with many pairs per SM by the stores to src, a line for each pair.  So up to 2^16
+// pairs go to one launch, a cluster of up to 16 CTAs that read each other's counts, and
+// more to two launches of up to 64 CTAs, the first of which counts (one / two launches, us:
+// 16384 pairs 6.6 / 9.4, 32768 pairs 6.3 / 8.9, 65536 pairs 7.9 / 9.1, 96000 pairs 9.5 / 9.1,
+// 131040 pairs 10.8 / 9.1; clusters of 8: 6.6, 7.5 and 11.0 at the first three; 30 pairs take
+// 4.5, 524168 pairs over 256 experts 15.0).  Ranking in the counting pass, so that the rows
 // need no further votes, gains 0.4 us at 30 pairs and loses 3.9 at 524168, where the votes
 // then no longer run under the stores.
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
 constexpr int PLAN_PAIRS = 2048;  // pairs of a chunk, at least
 constexpr int PLAN_CHUNKS = 64;
-constexpr int PLAN_CLUSTER = 8;   // chunks that one cluster takes, at most
+constexpr int PLAN_CLUSTER = 16;  // chunks that one cluster takes, at most
 constexpr int PLAN_REGS = 16;     // 32-pair steps of a warp's run, at most
-constexpr int PLAN_CLUSTER_PAIRS = 1 << 15;  // pairs that one cluster takes, at most
+constexpr int PLAN_CLUSTER_PAIRS = 1 << 16;  // pairs that one cluster takes, at most
 
 // (the layout holds at most 2^20 rows, and so pairs)
 static_assert(int64_t(PLAN_CHUNKS) * PLAN_WARPS * PLAN_REGS * 32 >= (1 << 20), "runs hold all pairs");
@@ -785,11 +786,9 @@ cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t
 {
     const int pairs = int(T * k);
     const bool one = pairs <= PLAN_CLUSTER_PAIRS;  // one cluster
-    const int64_t wanted = (pairs + PLAN_PAIRS - 1) / PLAN_PAIRS, most = one ? PLAN_CLUSTER : PLAN_CHUNKS;
-    const int chunks = int(wanted < most ? wanted : most);
     const size_t count_smem = size_t(E) * sizeof(int);
     const size_t place_smem = ((PLAN_WARPS + 4) * size_t(E) + 1) * sizeof(int);
-    static LaunchCache cache;
+    static LaunchCache cache;  // CTAs of the largest cluster that the GPU takes
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -801,10 +800,30 @@ cudaError_t launch_moe_plan(const int32_t *ids, int64_t T, int k, int E, int32_t
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(moe_plan_place_kernel<false>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(moe_plan_place_kernel<true>,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
-        cache.set(dev, 1);
+        cudaLaunchConfig_t q = {};
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = PLAN_CLUSTER;
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        q.gridDim = dim3(PLAN_CLUSTER);
+        q.blockDim = dim3(PLAN_THREADS);
+        q.dynamicSmemBytes = most_smem;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, moe_plan_place_kernel<true>, &q);
+        if (e != cudaSuccess)
+            return e;
+        cache.set(dev, n > 0 ? PLAN_CLUSTER : 8);  // 8 is portable
     }
+    const int64_t wanted = (pairs + PLAN_PAIRS - 1) / PLAN_PAIRS, most = one ? cache.get(dev) : PLAN_CHUNKS;
+    const int chunks = int(wanted < most ? wanted : most);
     const int rows = int(moe_plan_rows(T, k, E));
     int *hist = static_cast<int *>(workspace);
     if (one)

@@ -139,7 +139,8 @@ def test_route_rows_past_2_gb(dtype):
 @pytest.mark.parametrize("t,e,k,out", [
     (130000, 16, 8, False),   # nearly 2^20 pairs: every step of the warps' runs
     (300, 1024, 8, True), (1021, 1000, 16, True), (2341, 7, 7, True), (1 << 15, 1, 1, False),
-    (4096, 64, 8, True), (4097, 64, 8, True)])   # 2^15 pairs and a token more
+    (4096, 64, 8, True), (4097, 64, 8, True),
+    (8192, 128, 8, True), (8193, 128, 8, True), (2048, 1024, 32, True)])   # 2^16 pairs and a token more
 def test_plan_of_many_pairs(t, e, k, out):
     g = gen(7)
     _, ids = fb.fp8_moe_route(torch.randn(t, e, generator=g, device="cuda"), k)

@@ -61,7 +61,7 @@ def build_calls(force: bool = False) -> str:
     subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
                     "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
                     *[f"-I{i}" for i in inc], src, "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch",
-                    "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
+                    "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], check=True)
     os.replace(tmp, CALLS)
     return CALLS
 

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -103,8 +104,9 @@ struct Call {
     at::Tensor out(PyObject *o, at::ScalarType type, Shape shape)
     {
         if (!given(o))
-            return at::empty(at::IntArrayRef(shape),
-                             at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, dev)));
+            // (not through the dispatcher, which takes longer than the allocator)
+            return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(shape), type,
+                                                     at::Device(at::kCUDA, dev), std::nullopt));
         const at::Tensor &t = tensor(o);
         check(t, type, shape);
         return t;

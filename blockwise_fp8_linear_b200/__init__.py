@@ -198,9 +198,16 @@ def _refuse(items):
     return dev.index
 
 
-def _alloc(t, shape, dtype, device):
+def _alloc(t, shape, dtype, device, stream=None):
+    """t, or a new tensor.  With a stream it comes from the allocator's pool of that stream:
+    a block of the current stream's may still be read there by work queued before."""
     import torch
-    return torch.empty(*shape, dtype=dtype, device=device) if t is None else t
+    if t is not None:
+        return t
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _dims(M, N=None, K=None):
@@ -535,7 +542,7 @@ def fp8_linear_few(x, qw, sw, out=None, workspace=None, stream=None):
     L = lib()
     need = L.fp8_linear_few_workspace(M, K)
     with _on(dev):
-        out = _alloc(out, (M, N), torch.bfloat16, dev)
+        out = _alloc(out, (M, N), torch.bfloat16, dev, stream)
         if need:
             workspace = _workspace(workspace, need, dev, stream)
         _check(L.fp8_linear_few(x.data_ptr(), qw.data_ptr(), sw.data_ptr(), out.data_ptr(),
@@ -598,8 +605,8 @@ def fp8_moe_route(logits, k: int, renorm: bool = True, weights=None, ids=None, s
     dev = _validate([(logits, logits.dtype, (T, E), "logits"),
                      (weights, torch.float32, (T, k), "weights"), (ids, torch.int32, (T, k), "ids")])
     with _on(dev):
-        weights = _alloc(weights, (T, k), torch.float32, dev)
-        ids = _alloc(ids, (T, k), torch.int32, dev)
+        weights = _alloc(weights, (T, k), torch.float32, dev, stream)
+        ids = _alloc(ids, (T, k), torch.int32, dev, stream)
         _check(lib().fp8_moe_route(logits.data_ptr(), int(bf16), T, E, k, int(bool(renorm)),
                                    weights.data_ptr(), ids.data_ptr(), _stream(stream)),
                "fp8_moe_route")
@@ -622,7 +629,7 @@ def fp8_moe_route_bwd(dweights, weights, ids, logits, renorm: bool = True, dlogi
                      (logits, logits.dtype, (T, E), "logits"),
                      (dlogits, logits.dtype, (T, E), "dlogits")])
     with _on(dev):
-        dlogits = _alloc(dlogits, (T, E), logits.dtype, dev)
+        dlogits = _alloc(dlogits, (T, E), logits.dtype, dev, stream)
         _check(lib().fp8_moe_route_bwd(dweights.data_ptr(), weights.data_ptr(), ids.data_ptr(),
                                        logits.data_ptr(), int(bf16), T, E, k, int(bool(renorm)),
                                        dlogits.data_ptr(), _stream(stream)), "fp8_moe_route_bwd")
@@ -655,9 +662,9 @@ def fp8_moe_plan(ids, E: int, seg=None, row=None, src=None, workspace=None, stre
                      (row, torch.int32, (T, k), "row"), (src, torch.int32, (rows,), "src")])
     need = int(lib().fp8_moe_plan_workspace(T, E, k))
     with _on(dev):
-        seg = _alloc(seg, (E + 1,), torch.int32, dev)
-        row = _alloc(row, (T, k), torch.int32, dev)
-        src = _alloc(src, (rows,), torch.int32, dev)
+        seg = _alloc(seg, (E + 1,), torch.int32, dev, stream)
+        row = _alloc(row, (T, k), torch.int32, dev, stream)
+        src = _alloc(src, (rows,), torch.int32, dev, stream)
         workspace = _workspace(workspace, need, dev, stream)
         _check(lib().fp8_moe_plan(ids.data_ptr(), T, E, k, seg.data_ptr(), row.data_ptr(),
                                   src.data_ptr(), workspace.data_ptr(), _stream(stream)),
@@ -670,10 +677,7 @@ def _workspace(ws, need, dev, stream):
     call returns, so it has to come from the allocator's pool of the stream that uses it."""
     import torch
     if ws is None:
-        if stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=dev)
-        with torch.cuda.stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=dev)
+        return _alloc(None, (need,), torch.uint8, dev, stream)
     if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
         raise TypeError("workspace must be a uint8 tensor")
     if ws.dim() != 1 or ws.numel() < need:
@@ -716,7 +720,7 @@ def fp8_gemm_grouped(mode: int, a, sa, b, sb, seg, M: int, N: int, K: int, out=N
                      (b, torch.uint8, sh_b, "b"), (sb, torch.float32, sh_sb, "sb"),
                      (seg, torch.int32, (E + 1,), "seg"), (out, torch.bfloat16, sh_d, "out")])
     with _on(dev):
-        out = _alloc(out, sh_d, torch.bfloat16, dev)
+        out = _alloc(out, sh_d, torch.bfloat16, dev, stream)
         _check(lib().fp8_gemm_grouped(int(mode), a.data_ptr(), sa.data_ptr(), b.data_ptr(),
                                       sb.data_ptr(), seg.data_ptr(), E, out.data_ptr(), M, N, K,
                                       _stream(stream)), "fp8_gemm_grouped")
@@ -780,7 +784,7 @@ def fp8_moe_few(x, w1, s1, w2, s2, ids, weights, out=None, workspace=None, strea
                      (weights, torch.float32, (T, k), "weights"),
                      (out, torch.bfloat16, (T, H), "out")])
     with _on(dev):
-        out = _alloc(out, (T, H), torch.bfloat16, dev)
+        out = _alloc(out, (T, H), torch.bfloat16, dev, stream)
         workspace = _workspace(workspace, fp8_moe_few_workspace(T, k, H, I), dev, stream)
         _check(lib().fp8_moe_few(x.data_ptr(), w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
                                  s2.data_ptr(), ids.data_ptr(), weights.data_ptr(),

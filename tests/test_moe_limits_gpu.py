@@ -229,3 +229,32 @@ def test_overlapping_arguments_are_refused():
     both[0] = x
     y = fb.fp8_linear_few(both[0], square, scales, out=both[1])
     assert torch.equal(y, fb.fp8_linear_few(x, square, scales))
+
+
+def test_outputs_on_another_stream_take_no_block_of_the_current_one():
+    # work queued on the current stream may still read a block that Python has freed
+    x, w1, s1, w2, s2, ids, wt = a = make(gen(40), 64, 8, 2, 1024, 256)
+    logits = torch.randn(64, 1024, generator=gen(41), device="cuda")
+    lw, lids = fb.fp8_moe_route(logits, 32)
+    codes, sc = fb.fp8_quant_act(acts(gen(42), 256, 1024))
+    b, sb = fb.fp8_quant_act(acts(gen(43), 8 * 512, 1024))[0].view(8, 512, 1024), torch.ones(8, 4, 8, device="cuda")
+    seg = torch.tensor([0, 1, 2] + [2] * 6, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda **kw: fb.fp8_linear_few(x, w1[0], s1[0], **kw),
+                 lambda **kw: fb.fp8_moe_route(logits, 32, **kw),
+                 lambda **kw: fb.fp8_moe_route_bwd(lw, lw, lids, logits, **kw),
+                 lambda **kw: fb.fp8_moe_plan(lids, 1024, **kw),
+                 lambda **kw: fb.fp8_gemm_grouped(fb.FPROP, codes, sc, b, sb, seg, 256, 512, 1024, **kw),
+                 lambda **kw: fb.fp8_moe_few(*a, **kw)):
+        here = call()
+        here = here if isinstance(here, tuple) else (here,)
+        freed = {t.untyped_storage().data_ptr() for t in here}
+        want = [t.clone() for t in here]
+        torch.cuda.synchronize()
+        del here
+        there = call(stream=side)
+        there = there if isinstance(there, tuple) else (there,)
+        assert not freed & {t.untyped_storage().data_ptr() for t in there}
+        side.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(there, want))

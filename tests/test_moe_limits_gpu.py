@@ -258,3 +258,22 @@ def test_outputs_on_another_stream_take_no_block_of_the_current_one():
         assert not freed & {t.untyped_storage().data_ptr() for t in there}
         side.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(there, want))
+
+
+@pytest.mark.parametrize("t", [2, 5, 12, 40, 64])
+def test_a_token_without_finite_values_stays_alone(t):
+    # (its own results are unspecified)
+    a = make(gen(50 + t), t, 12, 3, 512, 384)
+    x, w1, s1 = a[:3]
+    a[5][t - 1] = -1                  # one that chooses nothing: zero whatever its values are
+    clean, layer_clean = fb.fp8_linear_few(x, w1[0], s1[0]), fb.fp8_moe_few(*a)
+    for value in (float("nan"), float("inf")):
+        for row in {0, t // 2, t - 1}:
+            bad = x.clone()
+            bad[row, 100:300] = value
+            rest = torch.arange(t, device="cuda") != row
+            assert torch.equal(fb.fp8_linear_few(bad, w1[0], s1[0])[rest], clean[rest])
+            y = fb.fp8_moe_few(bad, *a[1:])
+            assert torch.equal(y[rest], layer_clean[rest]) and (y[t - 1] == 0).all()
+    torch.cuda.synchronize()
+    assert fb.fp8bw_last_device_error() == 0

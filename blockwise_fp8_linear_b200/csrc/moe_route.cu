@@ -158,7 +158,8 @@ __device__ __forceinline__ float exp_neg(float d)
 // The k largest logits of a row, each lane's registers as in Row; a lane's register holds a
 // word whose order is theirs.  Nothing has to be taken out between two rounds: relative
 // to the last maximum, counting down modulo 2^32, what is below it comes before what is
-// not.
+// not.  Where nothing is below it, the count wraps and `last` climbs back to the largest
+// word: a round that does not lower `last` has found nothing.
 template <int NV> struct RowWords {
     uint32_t word[NV], last;
     // the next round's maximum distance, and this lane's
@@ -222,7 +223,8 @@ template <class T, int V, int NV> struct RowTop : RowWords<NV> {
 // FP32 logits: the rounds find the k largest keys, each lane noting the rounds that it won;
 // which register it was is looked up afterwards, once per lane and win (two or three times,
 // in place of k).  Equal logits among the choices show in there being more registers of at
-// least the last key than rounds; then the rounds are done again, one expert at a time.
+// least the last key than rounds (as there are, too, where a row without -inf runs out of
+// distinct values before k); then the rounds are done again, one expert at a time.
 template <int V, int NV> struct RowTop<float, V, NV> : RowWords<NV> {
     static constexpr bool OWN_ID = false;
     __device__ __forceinline__ int choose(const float (&v)[NV], int k, int lane, int32_t *ids,
@@ -234,12 +236,12 @@ template <int V, int NV> struct RowTop<float, V, NV> : RowWords<NV> {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             word[i] = order_key(v[i]);
-        uint32_t mine = 0u, wins = 0u, last = 0u;
+        uint32_t mine = 0u, wins = 0u, last = 0xFFFFFFFFu;  // (above every key)
         int left = 0;
         for (; left < k; ++left) {
             uint32_t best;
             const uint32_t far = this->descend(best);
-            if (this->last == 0u)
+            if (this->last == 0u || this->last >= last)
                 break;
             last = this->last;
             mine = lane >= left ? last : mine;

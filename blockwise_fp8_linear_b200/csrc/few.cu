@@ -241,10 +241,11 @@ __device__ __forceinline__ void few_store(const FewArgs &a, int r, int tile, int
 
 __device__ __forceinline__ void few_store_h(const FewArgs &a, int row, int tile, int lane, float4 h)
 {
-    float amax = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // the largest magnitude by its bits, whose order is that of the numbers with NaN above
+    // them all: a NaN reaches the scale (fmaxf would drop it), as in the quantizers
+    const uint32_t most = max(max(__float_as_uint(fabsf(h.x)), __float_as_uint(fabsf(h.y))),
+                              max(__float_as_uint(fabsf(h.z)), __float_as_uint(fabsf(h.w))));
+    const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
     // h is kept in FP32 up to its one rounding onto E4M3
     const float sc = __fdiv_rn(amax, 448.0f);
     uint32_t codes = 0u;

@@ -7,7 +7,10 @@
 // A function here handles the plain case, in which every argument is as it should be, on
 // the current device and stream, and returns NotImplemented for all others: the Python
 // function of the same name then names the fault, or makes the call on another device or
-// stream.  Nothing but the handling of arguments is done here.
+// stream.  Nothing but the handling of arguments is done here.  The interpreter lock is held
+// while arguments are looked at and released for what may wait: the allocation of outputs
+// (which may synchronize the device) and the call itself (a full launch queue; a host
+// function in the stream, ahead of the launch, may be waiting for the lock).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -18,6 +21,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <initializer_list>
 
@@ -75,6 +79,29 @@ bool truth(PyObject *o)
     return o == Py_True;
 }
 
+// Releases the interpreter lock for a scope.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// An output or workspace: the caller's, or one that make() allocates (without the lock).
+struct Out {
+    at::Tensor t;
+    at::ScalarType type;
+    int64_t shape[3];
+    int dims;
+    void make(c10::DeviceIndex dev)
+    {
+        // (not through the dispatcher, which takes longer than the allocator)
+        if (!t.defined())
+            t = at::Tensor(at::detail::empty_cuda(at::IntArrayRef(shape, size_t(dims)), type,
+                                                  at::Device(at::kCUDA, dev), std::nullopt));
+    }
+};
+
 // One call: the current device and stream, which its tensors have to be on.
 struct Call {
     c10::DeviceIndex dev = -1;  // asked for at the first tensor that is on a GPU
@@ -83,7 +110,6 @@ struct Call {
         if (given(stream))
             throw Other();
     }
-    void *stream() const { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
     void check(const at::Tensor &t, at::ScalarType type, at::IntArrayRef shape)
     {
         if (!t.is_cuda() || t.layout() != at::kStrided)
@@ -100,18 +126,17 @@ struct Call {
         check(t, type, shape);
         return t.data_ptr();
     }
-    // (an input has been looked at, so the device is known)
-    at::Tensor out(PyObject *o, at::ScalarType type, Shape shape)
+    Out out(PyObject *o, at::ScalarType type, Shape shape)
     {
-        if (!given(o))
-            // (not through the dispatcher, which takes longer than the allocator)
-            return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(shape), type,
-                                                     at::Device(at::kCUDA, dev), std::nullopt));
-        const at::Tensor &t = tensor(o);
-        check(t, type, shape);
-        return t;
+        Out r = {at::Tensor(), type, {}, int(shape.size())};
+        std::copy(shape.begin(), shape.end(), r.shape);
+        if (given(o)) {
+            r.t = tensor(o);
+            check(r.t, type, shape);
+        }
+        return r;
     }
-    at::Tensor workspace(PyObject *o, int64_t need)
+    Out workspace(PyObject *o, int64_t need)
     {
         if (!given(o))
             return out(o, at::kByte, {need});
@@ -119,7 +144,16 @@ struct Call {
         if (t.dim() != 1 || t.numel() < need)
             throw Other();
         check(t, at::kByte, t.sizes());
-        return t;
+        return {t, at::kByte, {t.numel()}, 1};
+    }
+    // Without the lock: allocates those that the caller has not given, then f(stream).
+    // (An input has been looked at, so the device is known.)
+    template <class F> int run(std::initializer_list<Out *> outs, F f) const
+    {
+        const Unlocked unlocked;
+        for (Out *o : outs)
+            o->make(dev);
+        return f(c10::cuda::getCurrentCUDAStream(dev).stream());
     }
 };
 
@@ -185,14 +219,16 @@ PyObject *linear_few(PyObject *, PyObject *const *args, Py_ssize_t n)
         const void *xp = c.in(a[0], at::kBFloat16, {M, K});
         const void *qp = c.in(a[1], at::kByte, {N, K});
         const void *sp = c.in(a[2], at::kFloat, {N / 128, K / 128});
-        at::Tensor y = c.out(a[3], at::kBFloat16, {M, N}), ws;
+        Out y = c.out(a[3], at::kBFloat16, {M, N}), ws = {};
         const int64_t need = abi.linear_few_workspace(M, K);
         if (need)
             ws = c.workspace(a[4], need);
-        return done(abi.linear_few(xp, static_cast<const uint8_t *>(qp), static_cast<const float *>(sp),
-                                   y.data_ptr(), M, N, K, need ? ws.data_ptr() : nullptr, c.stream()),
-                    "fp8_linear_few")
-                   ? THPVariable_Wrap(y) : nullptr;
+        const auto call = [&](void *stream) {
+            return abi.linear_few(xp, static_cast<const uint8_t *>(qp), static_cast<const float *>(sp),
+                                  y.t.data_ptr(), M, N, K, need ? ws.t.data_ptr() : nullptr, stream);
+        };
+        const int status = need ? c.run({&y, &ws}, call) : c.run({&y}, call);
+        return done(status, "fp8_linear_few") ? THPVariable_Wrap(y.t) : nullptr;
     });
 }
 
@@ -208,11 +244,12 @@ PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t n)
         require(choices(T, E, k));
         const void *lp = c.in(a[0], l.scalar_type(), {T, E});
         const bool renorm = truth(a[2]);
-        at::Tensor w = c.out(a[3], at::kFloat, {T, k}), ids = c.out(a[4], at::kInt, {T, k});
-        return done(abi.moe_route(lp, bf16, T, E, k, renorm, static_cast<float *>(w.data_ptr()),
-                                  static_cast<int32_t *>(ids.data_ptr()), c.stream()),
-                    "fp8_moe_route")
-                   ? tuple(w, ids) : nullptr;
+        Out w = c.out(a[3], at::kFloat, {T, k}), ids = c.out(a[4], at::kInt, {T, k});
+        const int status = c.run({&w, &ids}, [&](void *stream) {
+            return abi.moe_route(lp, bf16, T, E, k, renorm, static_cast<float *>(w.t.data_ptr()),
+                                 static_cast<int32_t *>(ids.t.data_ptr()), stream);
+        });
+        return done(status, "fp8_moe_route") ? tuple(w.t, ids.t) : nullptr;
     });
 }
 
@@ -229,12 +266,13 @@ PyObject *moe_route_bwd(PyObject *, PyObject *const *args, Py_ssize_t n)
         const void *dw = c.in(a[0], at::kFloat, {T, k}), *w = c.in(a[1], at::kFloat, {T, k});
         const void *ip = c.in(a[2], at::kInt, {T, k}), *lp = c.in(a[3], l.scalar_type(), {T, E});
         const bool renorm = truth(a[4]);
-        at::Tensor dl = c.out(a[5], l.scalar_type(), {T, E});
-        return done(abi.moe_route_bwd(static_cast<const float *>(dw), static_cast<const float *>(w),
-                                      static_cast<const int32_t *>(ip), lp, bf16, T, E, k, renorm,
-                                      dl.data_ptr(), c.stream()),
-                    "fp8_moe_route_bwd")
-                   ? THPVariable_Wrap(dl) : nullptr;
+        Out dl = c.out(a[5], l.scalar_type(), {T, E});
+        const int status = c.run({&dl}, [&](void *stream) {
+            return abi.moe_route_bwd(static_cast<const float *>(dw), static_cast<const float *>(w),
+                                     static_cast<const int32_t *>(ip), lp, bf16, T, E, k, renorm,
+                                     dl.t.data_ptr(), stream);
+        });
+        return done(status, "fp8_moe_route_bwd") ? THPVariable_Wrap(dl.t) : nullptr;
     });
 }
 
@@ -250,15 +288,16 @@ PyObject *moe_plan(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int64_t rows = abi.moe_plan_rows(T, E, k);
         require(rows > 0);
         const void *ip = c.in(a[0], at::kInt, {T, k});
-        at::Tensor seg = c.out(a[2], at::kInt, {E + 1}), row = c.out(a[3], at::kInt, {T, k});
-        at::Tensor src = c.out(a[4], at::kInt, {rows});
-        at::Tensor ws = c.workspace(a[5], abi.moe_plan_workspace(T, E, k));
-        return done(abi.moe_plan(static_cast<const int32_t *>(ip), T, E, k,
-                                 static_cast<int32_t *>(seg.data_ptr()),
-                                 static_cast<int32_t *>(row.data_ptr()),
-                                 static_cast<int32_t *>(src.data_ptr()), ws.data_ptr(), c.stream()),
-                    "fp8_moe_plan")
-                   ? tuple(seg, row, src) : nullptr;
+        Out seg = c.out(a[2], at::kInt, {E + 1}), row = c.out(a[3], at::kInt, {T, k});
+        Out src = c.out(a[4], at::kInt, {rows});
+        Out ws = c.workspace(a[5], abi.moe_plan_workspace(T, E, k));
+        const int status = c.run({&seg, &row, &src, &ws}, [&](void *stream) {
+            return abi.moe_plan(static_cast<const int32_t *>(ip), T, E, k,
+                                static_cast<int32_t *>(seg.t.data_ptr()),
+                                static_cast<int32_t *>(row.t.data_ptr()),
+                                static_cast<int32_t *>(src.t.data_ptr()), ws.t.data_ptr(), stream);
+        });
+        return done(status, "fp8_moe_plan") ? tuple(seg.t, row.t, src.t) : nullptr;
     });
 }
 
@@ -299,12 +338,13 @@ PyObject *gemm_grouped(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int64_t mode = integer(a[0]);
         require(mode >= FP8BW_FPROP && mode <= FP8BW_WGRAD);
         const Grouped g(c, mode, a + 1);
-        at::Tensor d = mode == FP8BW_WGRAD ? c.out(a[9], at::kBFloat16, {g.E, g.M, g.N})
-                                           : c.out(a[9], at::kBFloat16, {g.M, g.N});
-        return done(abi.gemm_grouped(int(mode), g.a, g.sa, g.b, g.sb, g.seg, g.E, d.data_ptr(), g.M,
-                                     g.N, g.K, c.stream()),
-                    "fp8_gemm_grouped")
-                   ? THPVariable_Wrap(d) : nullptr;
+        Out d = mode == FP8BW_WGRAD ? c.out(a[9], at::kBFloat16, {g.E, g.M, g.N})
+                                    : c.out(a[9], at::kBFloat16, {g.M, g.N});
+        const int status = c.run({&d}, [&](void *stream) {
+            return abi.gemm_grouped(int(mode), g.a, g.sa, g.b, g.sb, g.seg, g.E, d.t.data_ptr(), g.M,
+                                    g.N, g.K, stream);
+        });
+        return done(status, "fp8_gemm_grouped") ? THPVariable_Wrap(d.t) : nullptr;
     });
 }
 
@@ -316,9 +356,11 @@ PyObject *gemm_grouped_wgrad_acc32(PyObject *, PyObject *const *args, Py_ssize_t
         const Grouped g(c, FP8BW_WGRAD, a);
         require(given(a[8]));
         void *dw = c.in(a[8], at::kFloat, {g.E, g.M, g.N});
-        if (!done(abi.gemm_grouped_wgrad_acc32(g.a, g.sa, g.b, g.sb, g.seg, g.E,
-                                               static_cast<float *>(dw), g.M, g.N, g.K, c.stream()),
-                  "fp8_gemm_grouped_wgrad_acc32"))
+        const int status = c.run({}, [&](void *stream) {
+            return abi.gemm_grouped_wgrad_acc32(g.a, g.sa, g.b, g.sb, g.seg, g.E,
+                                                static_cast<float *>(dw), g.M, g.N, g.K, stream);
+        });
+        if (!done(status, "fp8_gemm_grouped_wgrad_acc32"))
             return nullptr;
         Py_INCREF(a[8]);
         return a[8];
@@ -342,13 +384,14 @@ PyObject *moe_few(PyObject *, PyObject *const *args, Py_ssize_t n)
         const void *ip = c.in(a[5], at::kInt, {T, k}), *wp = c.in(a[6], at::kFloat, {T, k});
         const int64_t need = abi.moe_few_workspace(T, k, H, I);
         require(need > 0);
-        at::Tensor y = c.out(a[7], at::kBFloat16, {T, H}), ws = c.workspace(a[8], need);
-        return done(abi.moe_few(xp, static_cast<const uint8_t *>(w1p), static_cast<const float *>(s1p),
-                                static_cast<const uint8_t *>(w2p), static_cast<const float *>(s2p),
-                                static_cast<const int32_t *>(ip), static_cast<const float *>(wp),
-                                y.data_ptr(), T, E, k, H, I, ws.data_ptr(), c.stream()),
-                    "fp8_moe_few")
-                   ? THPVariable_Wrap(y) : nullptr;
+        Out y = c.out(a[7], at::kBFloat16, {T, H}), ws = c.workspace(a[8], need);
+        const int status = c.run({&y, &ws}, [&](void *stream) {
+            return abi.moe_few(xp, static_cast<const uint8_t *>(w1p), static_cast<const float *>(s1p),
+                               static_cast<const uint8_t *>(w2p), static_cast<const float *>(s2p),
+                               static_cast<const int32_t *>(ip), static_cast<const float *>(wp),
+                               y.t.data_ptr(), T, E, k, H, I, ws.t.data_ptr(), stream);
+        });
+        return done(status, "fp8_moe_few") ? THPVariable_Wrap(y.t) : nullptr;
     });
 }
 

@@ -1,5 +1,5 @@
-"""Build ``libfp8bw.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and ``_calls.so``
-(the binding's compiled calls, against the installed torch) with g++.
+"""Build ``libfp8bw.so`` (the C-ABI library) in-tree with nvcc for sm_100a, and then, where
+torch is installed, ``_calls.so`` (the Python binding's compiled calls) with g++.
 
 Usage: ``python -m blockwise_fp8_linear_b200.build [--force] [--verbose]``.
 Rebuilds only when a source or header is newer than the library.  IEEE division and
@@ -8,6 +8,7 @@ no flush-to-zero are required for bit-exact quantization, so no fast-math flags.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -66,8 +67,7 @@ def build_calls(force: bool = False) -> str:
     return CALLS
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_calls(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(p) <= t for p in _deps()):
@@ -85,6 +85,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library first: C programs need neither torch nor its headers."""
+    build_library(force, verbose)
+    if importlib.util.find_spec("torch") is not None:
+        build_calls(force)
     return LIB
 
 

@@ -893,11 +893,14 @@ few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUte
 // beyond some tokens that takes longer than their weights take to arrive, and the codes
 // come from the quantizer's kernel instead, a launch more, whose time the next one's start
 // hides.  Measured (itself / codes): 8 tokens 5.0 / 6.1 us at 2048 x 2048 and 28.9 / 29.9 at
-// 12288 x 12288; 16 tokens 6.1 / 6.5, 10.2 / 9.3 (12288 x 2048) and 39.2 / 30.5; 32 tokens
-// 9.6 / 7.2 at 2048 x 2048.
+// 12288 x 12288; 16 tokens 5.6 / 5.7 (1024 x 1024), 6.3 / 6.1 (2048 x 2048), 7.1 / 6.9 (4096 x
+// 2048), 9.3 / 9.4 (4096 x 4096), 11.6 / 10.3 (12288 x 2048), 13.0 / 11.2 (2048 x 12288), 12.4
+// / 11.7 (8192 x 4096) and 39.2 / 30.5 (12288 x 12288); 9 tokens within 0.3 us at all of these
+// but 4096 x 4096 (8.3 / 9.1) and up to 1024 x 1024 (4.9 / 5.5); 32 tokens 9.6 / 7.2 at 2048 x
+// 2048.
 constexpr int FEW_QUANT_TOKENS = 8;        // at any size
-constexpr int FEW_QUANT_TOKENS_SMALL = 16; // of a weight below this many elements
-constexpr int64_t FEW_QUANT_SMALL = int64_t(1) << 25;
+constexpr int FEW_QUANT_TOKENS_SMALL = 16; // of a weight of at most this many elements
+constexpr int64_t FEW_QUANT_SMALL = int64_t(1) << 24;
 
 // CTAs per item: the split of the reduction that leaves an SM the least time, in blocks of
 // a CTA alone: two CTAs on an SM take 0.7 of their blocks' sum (each hides the other's
@@ -1017,7 +1020,7 @@ cudaError_t launch_linear_few(const void *x, int T, const uint8_t *qw, const flo
     a.N = int(N);
     a.K = int(K);
     a.KB = int(K / 128);
-    if (T <= FEW_QUANT_TOKENS || (T <= FEW_QUANT_TOKENS_SMALL && N * K < FEW_QUANT_SMALL))
+    if (T <= FEW_QUANT_TOKENS || (T <= FEW_QUANT_TOKENS_SMALL && N * K <= FEW_QUANT_SMALL))
         return run_few<FewCfg<FEW_LINEAR, 16>>(qw, N, nullptr, a, stream, num_sms);
     uint8_t *q = static_cast<uint8_t *>(workspace);
     float *s = reinterpret_cast<float *>(q + size_t(T) * K);

@@ -40,6 +40,20 @@ def test_linear_shapes(m, n, k):
     check_linear(acts(g, m, k), qw[0], sw[0])
 
 
+@pytest.mark.parametrize("m", [9, 12, 16])
+@pytest.mark.parametrize("n,k", [(4096, 4096), (4224, 4096), (12288, 2048), (2048, 12288)])
+def test_linear_where_the_codes_change_hands(m, n, k):
+    # weights about the size from which the quantizer's kernel makes the codes
+    g = gen(m + n)
+    qw, sw = weights(g, 1, n, k)
+    x = acts(g, m, k)
+    y = check_linear(x, qw[0], sw[0])
+    # fewer tokens are quantized in the kernel at every size: the same codes, other sums
+    a, w = dequant_rows(x[:8]), blocks64(qw[0], sw[0])
+    check_bf16(fb.fp8_linear_few(x[:8].contiguous(), qw[0], sw[0]), a @ w.t(), a.abs() @ w.abs().t(), k, "8 tokens")
+    assert y.shape == (m, n)
+
+
 def test_linear_values():
     """Zero rows and groups, scales at both ends of the range, outliers."""
     g = gen(4)

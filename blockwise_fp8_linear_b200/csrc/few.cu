@@ -34,13 +34,14 @@
 // theirs are not stored.  Every wait is bounded.
 //
 // Measured on the device, weights from HBM (one B200, 6.5 TB/s copy rate):
-//   linear  1 token 2048 x 2048 4.4 us; 7 tokens 2048 x 6144 7.2 us; 8 tokens 12288 x 2048
-//           9.4 us (2.7 TB/s); 1 token 12288 x 12288 28.8 us (5.3 TB/s)
-//   codes   61 tokens 12288 x 2048 13.8 us with the quantizer's launch (2.0 TB/s: 96 tiles on
-//           148 SMs); 64 tokens 12288 x 12288 42.8 us (3.6 TB/s)
-//   layer   128 experts of 2048 x 768, 8 choices: 1 token 21.8 us (start-up, join and
-//           combination are most of it); 8 tokens 59 us (4.0 TB/s); 40 tokens 111 us (5.1
-//           TB/s); 64 tokens 128 us (4.7 TB/s)
+//   linear  1 token 2048 x 2048 4.5 us; 7 tokens 2048 x 6144 7.0 us; 8 tokens 12288 x 2048
+//           9.3 us (2.7 TB/s: 96 tiles on 148 SMs); 1 token 12288 x 12288 29.0 us (5.2 TB/s)
+//   codes   61 tokens 12288 x 2048 13.7 us with the quantizer's launch (2.0 TB/s: 96 tiles on
+//           148 SMs, which a cluster of 3 does not fit); 64 tokens 12288 x 12288 43.2 us (3.6
+//           TB/s)
+//   layer   128 experts of 2048 x 768, 8 choices: 1 token 21.5 us (start-up, join and
+//           combination are most of it); 8 tokens 60 us (4.0 TB/s); 40 tokens 111 us (5.1
+//           TB/s); 64 tokens 127 us (4.7 TB/s)
 // The layer of many tokens is bound by HBM and by starts and ends.  At 40 tokens up's first
 // product is done after 11 us (the tokens' groups wait behind the first weights), and as an
 // SM takes whole items, 4.8 of them on average, up's SMs end between 59 and 77 us; down,

@@ -1019,11 +1019,15 @@ cudaError_t launch_gemm_wgrad_acc32(const uint8_t *a, const float *sa, const uin
 // Grouped GEMM: how many rows each expert has is known to the GPU alone, so the tile is
 // chosen by what the sizes lead to expect.  Large ones are bound as the dense GEMM is, by the
 // promotion of each block's partial sums, and compute the rows that fill each expert's last
-// block as well: fprop of 65536 pairs, 128 experts, N 1536, K 2048, 340 us (1.2 PFLOP/s of
-// the pairs' products; an eighth as many rows again are fill); dgrad of 16384 pairs, 32 experts, N 1024, K
-// 2048, 65 us; wgrad of 32768 pairs, 32 experts, 2048 x 1536, 235 us, each tile with a
-// reduction of 8 blocks on average and a reduce-add of 256 KB into L2 behind it.  Small ones
-// are bound by latency (1000 pairs, 16 experts, N = K = 1024: 8.5 us, 16.5 MB).
+// block, and with pairs of blocks the odd half of its last pair, as well.  Fprop of 65536
+// pairs, 128 experts, N 1536, K 2048: 308 to 366 us with the clock that power leaves (1.34 to
+// 1.13 PFLOP/s of the pairs' products), for 1.25 times as many rows; with 512 rows in every
+// expert, nothing to fill, 249 us, beside 216 us of the dense GEMM over the same rows, so
+// that the walk from expert to expert and their weights take 15%.  Dgrad of 16384 pairs, 32
+// experts, N 1024, K 2048: 55 to 65 us, 50 without fill, 45 dense.  Wgrad of 32768 pairs, 32
+// experts, 2048 x 1536, each tile with a reduction of 8 blocks on average: 181 us into BF16,
+// 226 to 245 into FP32, where a reduce-add of 256 KB into L2 follows each tile.  Small ones are
+// bound by latency (1000 pairs, 16 experts, N = K = 1024: 8.3 us, 16.5 MB).
 //
 // fprop, dgrad: each expert's last block is half full on average, so the blocks in use are
 // those there are less half an expert's each, and pairs of blocks waste another quarter

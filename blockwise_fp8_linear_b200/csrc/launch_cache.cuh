@@ -30,9 +30,15 @@ struct LaunchCache {
 #define FP8BW_PDL 1
 #endif
 // Programmatic stream serialization: the kernel may be launched while the previous
-// kernel in the stream is still finishing (every kernel of this library waits for
-// its predecessor with griddepcontrol.wait before touching memory), so launch
-// latency and prologue (barrier set-up, tensor-memory allocation) overlap that tail.
+// kernel in the stream is still finishing, so launch latency and prologue (barrier set-up,
+// tensor-memory allocation) overlap that tail.  Every kernel of this library lets its
+// successor start (griddepcontrol.launch_dependents) only after its own
+// griddepcontrol.wait.  So when a kernel starts, all work before its predecessor is
+// complete and visible, and what the predecessor itself reads and writes is not.  Before its
+// wait a kernel may therefore read what was written ahead of its predecessor, and only if
+// it knows that one: the down and codes forms of the few-token kernel, whose predecessor is
+// up or a quantizer of the same call, read ids, weights and weight scales there.  All others
+// wait before they touch memory.
 inline void set_pdl(cudaLaunchAttribute &a)
 {
     a.id = cudaLaunchAttributeProgrammaticStreamSerialization;

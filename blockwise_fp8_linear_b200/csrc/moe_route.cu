@@ -301,10 +301,11 @@ template <int V, int NV> struct RowTop<float, V, NV> : RowWords<NV> {
 // weights[t][j], ids[t][j] for the k largest logits of row t, largest first, ties to
 // the lowest expert.  One warp per token, k rounds of RowTop; lane j keeps choice j.
 // Statistics in FP32.  Bound by the integer unit (71% busy at 65521 x 256 with 8 choices): a
-// round takes a subtraction and a maximum per register.  That size takes 27.0 us in BF16
-// (1.4 TB/s) and 38.7 us in FP32 (1.8 TB/s), whose registers are twice the bytes; 8192 x 128
-// in FP32 5.5 us.  (A warp per row: half a warp would save nothing, the registers' work
-// being the same.)  Tried: differences by multiply-adds and maxima of three, 30.5 us.
+// round takes a subtraction and a maximum per register.  That size takes 26.9 us in BF16
+// (1.4 TB/s) and 39.2 us in FP32 (1.8 TB/s), whose registers are twice the bytes, 2 us more
+// with the softmax over all; 8192 x 128 in FP32 5.8 us (logits from L2 or from HBM alike).
+// (A warp per row: half a warp would save nothing, the registers' work being the same.)
+// Tried: differences by multiply-adds and maxima of three, 30.5 us in BF16.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int renorm,
@@ -353,8 +354,9 @@ moe_route_kernel(const T *__restrict__ logits, int64_t rows, int E, int k, int r
 // is written, first the row without its choices, then these.  A choice with an id
 // outside [0, E) takes no part.  One warp per token, in FP32, rounded once to the logits'
 // type.  The row written, and read for the softmax over all: 65521 x 256 with 8 choices in
-// FP32 24.8 us (5.7 TB/s) and 18.9 us renormalized (3.9 TB/s); in BF16 20.8 and 15.0 us, bound
-// by issue slots (the exponentials and the row's way through shared memory).
+// FP32 24.5 us (5.8 TB/s) and 18.1 us renormalized (4.0 TB/s); in BF16 20.4 and 14.3 us, bound
+// by issue slots (the exponentials and the row's way through shared memory).  These are with
+// logits and gradient in HBM; in L2 24.2, 13.7, 20.1 and 11.2 us.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict__ weights,
@@ -478,7 +480,7 @@ moe_route_bwd_kernel(const float *__restrict__ dweights, const float *__restrict
 // more to two launches of up to 64 CTAs, the first of which counts (one / two launches, us:
 // 16384 pairs 6.6 / 9.4, 32768 pairs 6.3 / 8.9, 65536 pairs 7.9 / 9.1, 96000 pairs 9.5 / 9.1,
 // 131040 pairs 10.8 / 9.1; clusters of 8: 6.6, 7.5 and 11.0 at the first three; 30 pairs take
-// 4.5, 524168 pairs over 256 experts 15.0).  Ranking in the counting pass, so that the rows
+// 4.5, 524168 pairs over 256 experts 15.2).  Ranking in the counting pass, so that the rows
 // need no further votes, gains 0.4 us at 30 pairs and loses 3.9 at 524168, where the votes
 // then no longer run under the stores.
 constexpr int PLAN_WARPS = 32;

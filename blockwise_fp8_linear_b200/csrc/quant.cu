@@ -199,7 +199,7 @@ quant_tile_kernel(const __grid_constant__ CUtensorMap tmX, int64_t M, int64_t K,
     const int rsub = t >> 4, sub = t & 15;
 
     pdl_wait();               // X (and the output buffers) are free of the previous kernel
-    pdl_launch_dependents();
+    pdl_launch_dependents();  // (not earlier: the few-token linear reads weights before its wait)
     if (t == 0) {
         mbar_init(&bar, 1);
         abort_flag = 0;

@@ -258,6 +258,12 @@ int fp8_moe_route(const void *logits, int bf16, int64_t T, int64_t E, int64_t k,
  * G = sum_j g_j,  dlogits = [chosen] g - p G, where p is the softmax over the chosen
  * experts (renorm; zero elsewhere) or over all.  weights, ids and logits are those of
  * the forward call; dlogits [T][E] has the type of logits and is written whole.
+ * A choice whose id the caller has since put outside [0, E) takes no part, and nor does its
+ * expert's logit in a softmax over the chosen (to drop a choice there, leave its id and
+ * give it dweights 0).  The softmax over all is taken from the first choice, which is the
+ * largest of the forward call: p = w_0 exp(l - l_0), or anew where that one is left out.
+ * With the choices in another order that is as good as w_0 (not if it has underflowed) and
+ * exp(l - l_0) are.
  */
 int fp8_moe_route_bwd(const float *dweights, const float *weights, const int32_t *ids,
                       const void *logits, int bf16, int64_t T, int64_t E, int64_t k, int renorm,
@@ -314,7 +320,8 @@ int fp8_gemm_grouped_wgrad_acc32(const uint8_t *a, const float *sa, const uint8_
  * weights are read once, sums are FP32 and y is rounded to BF16 once.
  *   x [T][H] BF16
  *   w1 [E][2I][H], s1 [E][2I/128][H/128]     w2 [E][H][I], s2 [E][H/128][I/128]
- *     (fp8_quant_weight of the matrices stacked by expert)
+ *     (fp8_quant_weight of the matrices stacked by expert; a call of it takes at most
+ *     FP8BW_MAX_DIM rows, and its scales and codes of further experts simply follow)
  *   ids, weights [T][k] as from fp8_moe_route; a token that names an expert twice gives
  *     it the sum of the two weights; one whose choices are all left out gets y = 0
  *   y [T][H] BF16, written, never read
